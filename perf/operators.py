@@ -220,7 +220,7 @@ def _step(s):
     op, lens = c["op"], s["lens"]
     if op == "prefill":
         return step.PrefillStep(s["k"], s["v"], s["offsets"], max(lens), sum(lens), c["hq"], _roles(c), c["sink"], c["window"],
-                                s["scale"], max_total_q=s["q"].shape[0], max_new=max(s["new"]))
+                                s["scale"], s["q"].shape[0])
     if op == "prefix":
         return step.PrefixDecodeStep(s["pk"], s["pv"], s["p_offsets"], max(s["plens"]), sum(s["plens"]), s["k"], s["v"],
                                      s["offsets"], max(lens), sum(lens), c["hq"], s["scale"], seq_start=s["seq_start"])
