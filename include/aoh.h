@@ -161,7 +161,12 @@ typedef enum {
   AOH_KERNEL_SELECT_CLUSTER = 14, /* select: one cluster per row, keys on chip      */
   AOH_KERNEL_SELECT_RESOLVE = 15, /* select: exact threshold and chunk offsets per row */
   AOH_KERNEL_FLASH_MERGE = 16,  /* split-K combine of rows with many splits           */
-  AOH_KERNEL_KINDS = 17
+  AOH_KERNEL_ROLE_PREFILL = 17, /* new tokens attending by head role                  */
+  AOH_KERNEL_PREFIX_DECODE = 18, /* decode over a shared prefix                      */
+  AOH_KERNEL_ACCUM_MERGE = 19,  /* accumulated weights: combine and weights of a row  */
+  AOH_KERNEL_EVICT_KEY = 20,    /* eviction: scores of the selection                 */
+  AOH_KERNEL_EVICT_COPY = 21,   /* eviction: kept rows moved to the other cache      */
+  AOH_KERNEL_KINDS = 22
 } aoh_kernel_kind;
 
 /*
@@ -451,6 +456,143 @@ aoh_status aoh_kv_append(const void* q_new, int32_t n_q_heads, const void* k_new
                          double theta, const aoh_kv_cache* kv, const aoh_kv_cache* ring,
                          const int32_t* idom, int32_t n_dom, int32_t* lengths, void* q_out,
                          void* stream);
+
+/*
+ * aoh_kv_append_at -- aoh_kv_append for a cache whose rows have been thinned out
+ * (aoh_cache_evict), where a token's slot is no longer its position: the new
+ * token's rows go to slot lengths[b] of its region, its key and query are
+ * rotated to position positions[b], and both counters advance by one.
+ *   kv         a linear cache that stores every KV head
+ *   positions  device int32 [B], >= 0
+ * Other arguments, refusals and device checks as for aoh_kv_append; a sequence
+ * whose region is full or whose position is negative is left unchanged (both
+ * counters included; device check 4).
+ */
+aoh_status aoh_kv_append_at(const void* q_new, int32_t n_q_heads, const void* k_new, const void* v_new,
+                            double theta, const aoh_kv_cache* kv, const int32_t* idom, int32_t n_dom,
+                            int32_t* lengths, int32_t* positions, void* q_out, void* stream);
+
+/*
+ * aoh_stream_prefill -- attention of many new tokens at once by head role: a
+ * prompt, a chunk of one, or single tokens (AoH summary, Metodologia section 4:
+ * retrieval heads see the whole past, streaming heads a sink plus a recent
+ * window).  The new tokens' K / V rows are already in the cache: sequence b has
+ * n_b = q_offsets[b+1] - q_offsets[b] query rows, its last n_b positions.  Row i
+ * of them stands at p = L_b - n_b + i and sees
+ *   DENSE:   [0, p]
+ *   STREAM:  [0, min(sink, p + 1)) together with [max(0, p + 1 - window), p]
+ * (what aoh_stream_decode attends to with L = p + 1);
+ *   out[row][h] = sum over seen t of softmax_t(scale * q_h . k_t) * v_t.
+ *   q          device bf16 [total_q][n_q_heads][d], contiguous, already rotated
+ *   kv         linear cache (a ring is refused)
+ *   q_offsets  device int32 [B + 1], non-decreasing, q_offsets[0] = 0
+ *   total_q    rows of q and out; rows from q_offsets[B] on (a padded batch)
+ *              are neither read nor written.  q_offsets[B] <= total_q
+ *              (device check 1 otherwise, rows past total_q skipped)
+ *   roles      host uint8 [Hkv] (required); rows of SPARSE heads, and of heads the
+ *              cache does not store, are left as they are
+ *   scale      finite; sink, window >= 0
+ *   out        device bf16 [total_q][n_q_heads][d], 16-byte aligned: the softmax
+ *              and its sums are fp32, the weights enter the product with V as
+ *              bf16, the result is rounded once.  bf16, unlike the decode calls,
+ *              because a prompt's output is the next product's bf16 operand
+ *   workspace  device, 256-byte aligned, >= aoh_stream_prefill_workspace_size
+ *              bytes (any contents; 0 bytes: may be NULL)
+ * A row that sees nothing (n_b > L_b, or sink = window = 0) gives zeros.
+ * K and V of positions [0, L_b) must be finite; slots past L_b may hold anything.
+ * n_q_heads / n_kv_heads <= 32; batch <= 65535.
+ */
+aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv,
+                              const int32_t* q_offsets, int32_t total_q, const uint8_t* roles,
+                              int32_t sink, int32_t window, float scale, void* out,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads, int32_t total_q,
+                                         const uint8_t* roles, int32_t sink, int32_t window);
+
+/*
+ * aoh_prefix_decode -- one decode step of a batch whose sequences share long
+ * prefixes (a system prompt, a document, samples of one prompt): the shared
+ * tokens are stored once and read once for all their sequences.
+ *   prefix     linear cache of the prefixes: "sequence" i of it is prefix i
+ *              (batch = number of prefixes NP >= 1)
+ *   seq_start  device int32 [NP + 1], non-decreasing, seq_start[0] = 0,
+ *              seq_start[NP] = B: sequences [seq_start[i], seq_start[i+1])
+ *              continue prefix i (an empty range is allowed).  NULL: NP = 1 and
+ *              every sequence continues it.  A sequence that no range holds
+ *              attends to its own tokens only (device check 1)
+ *   kv         linear cache of the sequences' own tokens (L_b >= 0), same n_kv_heads
+ *              and head_dim, storing the same heads
+ *   q          device bf16 [B][n_q_heads][d]
+ *   out        device fp32 [B][n_q_heads][d]:
+ *              sum over the P_i prefix tokens and the L_b own tokens of
+ *              softmax(scale * q_h . k_t) * v_t; zeros when there is no token
+ *   workspace  device, 256-byte aligned, >= aoh_prefix_decode_workspace_size
+ *              bytes, zero-filled once before its first use
+ * K and V of held positions must be finite; slots past a length may hold anything.
+ * Heads that the caches do not store are left as they are.  n_q_heads /
+ * n_kv_heads <= 32; batch <= 65535.
+ */
+aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache* prefix,
+                             const int32_t* seq_start, const aoh_kv_cache* kv, float scale, float* out,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+size_t aoh_prefix_decode_workspace_size(const aoh_kv_cache* prefix, const aoh_kv_cache* kv,
+                                        int32_t n_q_heads);
+
+/*
+ * aoh_accum_decode -- decode attention over the whole cache [0, L_b) that also
+ * accumulates the attention weight each cached token receives:
+ *   out[b][h]      = sum over t of w_ht v_t,  w_ht = softmax_t(scale * q_h . k_t)
+ *   mass_out[g][t] = decay * mass_in[g][t] + sum over q heads h of group g of w_ht
+ * (the group is summed as in aoh_tip_score).  The mass ranks the tokens for
+ * aoh_cache_evict.
+ *   kv         linear cache; heads it does not store are skipped
+ *   decay      finite (1: a plain sum)
+ *   mass_in    device fp32 [Hkv][total_tokens] (layout of aoh_tip_score's scores), or
+ *              NULL (zeros)
+ *   mass_out   same layout, may be mass_in itself; entries of tokens outside every
+ *              [0, L_b) are left as they are
+ *   out        device fp32 [B][n_q_heads][d], 16-byte aligned
+ *   workspace  device, 256-byte aligned, >= aoh_accum_decode_workspace_size
+ *              bytes, zero-filled once before its first use
+ * n_q_heads / n_kv_heads <= 32; batch <= 65535.
+ */
+aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, float scale,
+                            float decay, const float* mass_in, float* mass_out, float* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads);
+
+/*
+ * aoh_cache_evict -- keep the tokens that attention has used.  Of the L_b
+ * positions of every (sequence, KV head) the call keeps n = min(budget, L_b): the
+ * first `sink`, the last `recent`, and of the others those with the largest
+ * mass (equal: the lower position; a NaN counts as the smallest).  Each head
+ * keeps positions of its own.  The kept rows are written, in position order, to
+ * slots 0 .. n - 1 of the sequence's region in another cache, from which any
+ * decode call goes on (keys keep the rotation of their original positions).
+ *   src        linear cache; mass: device fp32 [Hkv][src->total_tokens]
+ *   budget     >= 1; sink, recent >= 0 with sink + recent <= budget
+ *   dst        linear cache, same batch / n_kv_heads / head_dim, storing the same
+ *              heads, in memory apart from src (overlapping address ranges are
+ *              refused).  Its lengths field and k_dom are not used
+ *   dst_lengths  device int32 [B], written: n (usually dst's lengths array)
+ *   dst_mass   device fp32 [Hkv][dst->total_tokens] or NULL: the kept rows' mass,
+ *              zeros in the rest of the sequence's region
+ *   idx, count device int32 [B][Hkv][budget] and [B][Hkv]: the kept positions,
+ *              ascending, -1 padded, and n (layouts of aoh_topk_select)
+ *   workspace  device, 256-byte aligned, >= aoh_cache_evict_workspace_size bytes,
+ *              zero-filled once before its first use
+ * A sequence whose kept rows do not fit its region in dst is not copied and gets
+ * length 0 (device check 4).  batch <= 65535.  Rows up to 4 M positions.
+ */
+aoh_status aoh_cache_evict(const aoh_kv_cache* src, const float* mass, int32_t budget, int32_t sink,
+                           int32_t recent, const aoh_kv_cache* dst, int32_t* dst_lengths,
+                           float* dst_mass, int32_t* idx, int32_t* count, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+size_t aoh_cache_evict_workspace_size(const aoh_kv_cache* src);
 
 /*
  * aoh_head_classify -- the AoH offline head classifier on frozen projection

@@ -28,6 +28,9 @@ EXPORTS = (
     "aoh_shared_index_step", "aoh_shared_index_step_workspace_size", "aoh_stream_decode_noalloc",
     "aoh_launch_counts", "aoh_record_launch_events", "aoh_kv_append", "aoh_head_classify",
     "aoh_head_classify_workspace_size", "aoh_topk_select_workspace_size", "aoh_decode_step",
+    "aoh_kv_append_at", "aoh_stream_prefill", "aoh_stream_prefill_workspace_size", "aoh_prefix_decode",
+    "aoh_prefix_decode_workspace_size", "aoh_accum_decode", "aoh_accum_decode_workspace_size", "aoh_cache_evict",
+    "aoh_cache_evict_workspace_size",
     "aoh_decode_step_workspace_size", "aoh_offload_split", "aoh_offload_decode", "aoh_offload_decode_workspace_size",
 )
 NO_SLOT = 255  # head_slot entry of a KV head a cache does not store
@@ -37,7 +40,8 @@ KERNELS = ("tip_score_kernel", "select_hist_kernel", "sparse_row_kernel", "flash
            "pack_dominant_kernel", "kv_append_kernel", "gram_kernel", "gram_reduce_kernel", "spectrum_kernel",
            "group_roles_kernel", "offload_stage_kernel", "offload_split_kernel", "select_chunk_kernel",
            "select_write_kernel", "select_cluster_kernel",
-           "select_resolve_kernel", "flash_merge_kernel")
+           "select_resolve_kernel", "flash_merge_kernel", "role_prefill_kernel", "prefix_decode_kernel",
+           "accum_merge_kernel", "evict_key_kernel", "evict_copy_kernel")
 
 
 class AohError(RuntimeError):
@@ -107,6 +111,15 @@ def lib() -> ctypes.CDLL:
             "aoh_shared_index_step_workspace_size": (SZ, [KVP, I32, I32, I32]),
             "aoh_stream_decode_noalloc": (ctypes.c_int, [P, I32, KVP, P, I32, I32, F32, P, P]),
             "aoh_kv_append": (ctypes.c_int, [P, I32, P, P, ctypes.c_double, KVP, KVP, P, I32, P, P, P]),
+            "aoh_kv_append_at": (ctypes.c_int, [P, I32, P, P, ctypes.c_double, KVP, P, I32, P, P, P, P]),
+            "aoh_stream_prefill": (ctypes.c_int, [P, I32, KVP, P, I32, P, I32, I32, F32, P, P, SZ, P]),
+            "aoh_stream_prefill_workspace_size": (SZ, [KVP, I32, I32, P, I32, I32]),
+            "aoh_prefix_decode": (ctypes.c_int, [P, I32, KVP, P, KVP, F32, P, P, SZ, P]),
+            "aoh_prefix_decode_workspace_size": (SZ, [KVP, KVP, I32]),
+            "aoh_accum_decode": (ctypes.c_int, [P, I32, KVP, F32, F32, P, P, P, P, SZ, P]),
+            "aoh_accum_decode_workspace_size": (SZ, [KVP, I32]),
+            "aoh_cache_evict": (ctypes.c_int, [KVP, P, I32, I32, I32, KVP, P, P, P, P, P, SZ, P]),
+            "aoh_cache_evict_workspace_size": (SZ, [KVP]),
             "aoh_head_classify": (ctypes.c_int, [P, P, I32, I32, I32, I32, I32, P, P, P, P, SZ, P]),
             "aoh_head_classify_workspace_size": (SZ, [I32, I32, I32, I32]),
             "aoh_offload_split": (ctypes.c_int, [KVP, P, I32, P, I32, P, P]),
@@ -137,8 +150,8 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> Optional[int]:
 
 
 def _host_u8(arr) -> Optional[ctypes.Array]:
-    if arr is None:
-        return None
+    if arr is None or isinstance(arr, ctypes.Array):
+        return arr
     vals = [int(x) for x in (arr.tolist() if hasattr(arr, "tolist") else arr)]
     return (ctypes.c_uint8 * len(vals))(*vals)
 
@@ -356,6 +369,120 @@ def kv_append(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.T
         _ptr(q_new), 0 if q_new is None else q_new.shape[-2], _ptr(k_new), _ptr(v_new), float(theta),
         None if kv is None else ctypes.byref(kv), None if ring is None else ctypes.byref(ring), _ptr(idom),
         int(n_dom), _ptr(lengths), _ptr(q_out), _stream(stream)))
+
+
+def _want(fn: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, *shape) -> None:
+    """t is a contiguous tensor of this type and shape on the current device (None entries: any size)."""
+    if t is None or t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or any(
+            n is not None and m != n for m, n in zip(t.shape, shape)):
+        got = "None" if t is None else f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}"
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {shape}, got {got}")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _want_ws(fn: str, ws: Optional[torch.Tensor]) -> None:
+    if ws is None or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device.type != "cuda" or (
+            ws.device.index != torch.cuda.current_device()):
+        raise ValueError(f"{fn}: the workspace must be a contiguous uint8 tensor on the current device")
+
+
+def kv_append_at(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor, theta: float, kv: KVCache,
+                 idom: Optional[torch.Tensor], n_dom: int, lengths: torch.Tensor, positions: torch.Tensor,
+                 q_out: Optional[torch.Tensor], stream=None) -> None:
+    """Append every sequence's token at slot lengths[b], rotated to positions[b]; both advance (aoh_kv_append_at)."""
+    fn, d = "aoh_kv_append_at", kv.head_dim
+    _want(fn, "k_new", k_new, torch.bfloat16, kv.batch, kv.n_kv_heads, d)
+    _want(fn, "v_new", v_new, torch.bfloat16, kv.batch, kv.n_kv_heads, d)
+    _want(fn, "lengths", lengths, torch.int32, kv.batch)
+    _want(fn, "positions", positions, torch.int32, kv.batch)
+    if q_new is not None:
+        _want(fn, "q_new", q_new, torch.bfloat16, kv.batch, None, d)
+        _want(fn, "q_out", q_out, torch.bfloat16, *q_new.shape)
+    _check(fn, lib().aoh_kv_append_at(
+        _ptr(q_new), 0 if q_new is None else q_new.shape[-2], _ptr(k_new), _ptr(v_new), float(theta),
+        ctypes.byref(kv), _ptr(idom), int(n_dom), _ptr(lengths), _ptr(positions), _ptr(q_out), _stream(stream)))
+
+
+def stream_prefill_workspace_size(kv: KVCache, n_q_heads: int, total_q: int, roles, sink: int, window: int) -> int:
+    r = _host_u8(roles)
+    return int(lib().aoh_stream_prefill_workspace_size(ctypes.byref(kv), n_q_heads, total_q,
+                                                       ctypes.cast(r, ctypes.c_void_p), sink, window))
+
+
+def stream_prefill(q: torch.Tensor, kv: KVCache, q_offsets: torch.Tensor, roles, sink: int, window: int, scale: float,
+                   out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Attention of each sequence's new tokens by head role (aoh_stream_prefill); q, out bf16 [rows, Hq, d]."""
+    fn = "aoh_stream_prefill"
+    _want(fn, "q", q, torch.bfloat16, None, None, kv.head_dim)
+    _want(fn, "out", out, torch.bfloat16, *q.shape)
+    _want(fn, "q_offsets", q_offsets, torch.int32, kv.batch + 1)
+    _want_ws(fn, ws)
+    r = _host_u8(roles)
+    if r is not None and len(r) != kv.n_kv_heads:
+        raise ValueError(f"{fn}: {len(r)} roles for {kv.n_kv_heads} KV heads")
+    _check(fn, lib().aoh_stream_prefill(
+        q.data_ptr(), q.shape[1], ctypes.byref(kv), q_offsets.data_ptr(), q.shape[0], ctypes.cast(r, ctypes.c_void_p),
+        sink, window, float(scale), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+def prefix_decode_workspace_size(prefix: KVCache, kv: KVCache, n_q_heads: int) -> int:
+    return int(lib().aoh_prefix_decode_workspace_size(ctypes.byref(prefix), ctypes.byref(kv), n_q_heads))
+
+
+def prefix_decode(q: torch.Tensor, prefix: KVCache, seq_start: Optional[torch.Tensor], kv: KVCache, scale: float,
+                  out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Decode over a shared prefix and each sequence's own tokens (aoh_prefix_decode)."""
+    fn = "aoh_prefix_decode"
+    _want(fn, "q", q, torch.bfloat16, kv.batch, None, kv.head_dim)
+    _want(fn, "out", out, torch.float32, *q.shape)
+    if seq_start is not None:
+        _want(fn, "seq_start", seq_start, torch.int32, prefix.batch + 1)
+    _want_ws(fn, ws)
+    _check(fn, lib().aoh_prefix_decode(
+        q.data_ptr(), q.shape[1], ctypes.byref(prefix), _ptr(seq_start), ctypes.byref(kv), float(scale),
+        out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+def accum_decode_workspace_size(kv: KVCache, n_q_heads: int) -> int:
+    return int(lib().aoh_accum_decode_workspace_size(ctypes.byref(kv), n_q_heads))
+
+
+def accum_decode(q: torch.Tensor, kv: KVCache, scale: float, decay: float, mass_in: Optional[torch.Tensor],
+                 mass_out: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """Decode over the whole cache; mass_out = decay * mass_in + the group's attention weights (aoh_accum_decode)."""
+    fn = "aoh_accum_decode"
+    _want(fn, "q", q, torch.bfloat16, kv.batch, None, kv.head_dim)
+    _want(fn, "out", out, torch.float32, *q.shape)
+    if mass_in is not None:
+        _want(fn, "mass_in", mass_in, torch.float32, kv.n_kv_heads, kv.total_tokens)
+    _want(fn, "mass_out", mass_out, torch.float32, kv.n_kv_heads, kv.total_tokens)
+    _want_ws(fn, ws)
+    _check(fn, lib().aoh_accum_decode(
+        q.data_ptr(), q.shape[1], ctypes.byref(kv), float(scale), float(decay), _ptr(mass_in), mass_out.data_ptr(),
+        out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+
+
+def cache_evict_workspace_size(src: KVCache) -> int:
+    return int(lib().aoh_cache_evict_workspace_size(ctypes.byref(src)))
+
+
+def cache_evict(src: KVCache, mass: torch.Tensor, budget: int, sink: int, recent: int, dst: KVCache,
+                dst_lengths: torch.Tensor, dst_mass: Optional[torch.Tensor], idx: torch.Tensor, count: torch.Tensor,
+                ws: torch.Tensor, stream=None) -> None:
+    """Keep the first, the last and the heaviest rows of every head, moved to another cache (aoh_cache_evict)."""
+    fn = "aoh_cache_evict"
+    _want(fn, "mass", mass, torch.float32, src.n_kv_heads, src.total_tokens)
+    _want(fn, "dst_lengths", dst_lengths, torch.int32, src.batch)
+    if dst_mass is not None:
+        _want(fn, "dst_mass", dst_mass, torch.float32, dst.n_kv_heads, dst.total_tokens)
+    _want(fn, "idx", idx, torch.int32, src.batch, src.n_kv_heads, budget)
+    _want(fn, "count", count, torch.int32, src.batch, src.n_kv_heads)
+    _want_ws(fn, ws)
+    _check(fn, lib().aoh_cache_evict(
+        ctypes.byref(src), mass.data_ptr(), int(budget), int(sink), int(recent), ctypes.byref(dst),
+        dst_lengths.data_ptr(), _ptr(dst_mass), idx.data_ptr(), count.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream(stream)))
 
 
 def head_classify_workspace_size(d_model: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:

@@ -11,11 +11,15 @@
 #include <mutex>
 
 #include "aoh.h"
+#include "accum_decode.cuh"
+#include "cache_evict.cuh"
 #include "device_common.cuh"
 #include "flash_gather.cuh"
 #include "head_classify.cuh"
 #include "kv_append.cuh"
 #include "offload.cuh"
+#include "prefix_decode.cuh"
+#include "role_prefill.cuh"
 #include "select_cluster.cuh"
 #include "select_hist.cuh"
 #include "sparse_row.cuh"
@@ -1299,9 +1303,9 @@ aoh_status aoh_shared_index_step(const void* q_index, const void* q_layers, int3
   return launch_fd(fp, kv->head_dim, geo.nqp, n_listed, kv->batch, st, true);
 }
 
-aoh_status aoh_kv_append(const void* q_new, int32_t n_q_heads, const void* k_new, const void* v_new, double theta,
-                         const aoh_kv_cache* kv, const aoh_kv_cache* ring, const int32_t* idom, int32_t n_dom,
-                         int32_t* lengths, void* q_out, void* stream) {
+static aoh_status append_tokens(const void* q_new, int32_t n_q_heads, const void* k_new, const void* v_new, double theta,
+                                const aoh_kv_cache* kv, const aoh_kv_cache* ring, const int32_t* idom, int32_t n_dom,
+                                int32_t* lengths, int32_t* positions, void* q_out, void* stream) {
   if (!kv && !ring) return AOH_ERR_INVALID_ARG;
   aoh_status s;
   if (kv) {
@@ -1335,6 +1339,7 @@ aoh_status aoh_kv_append(const void* q_new, int32_t n_q_heads, const void* k_new
   ap.v_new = static_cast<const uint16_t*>(v_new);
   ap.q_out = static_cast<uint16_t*>(q_out);
   ap.lengths = lengths;
+  ap.positions = positions;
   ap.B = any->batch;
   ap.Hq = q_new ? n_q_heads : 0;
   ap.Hkv = any->n_kv_heads;
@@ -1371,6 +1376,21 @@ aoh_status aoh_kv_append(const void* q_new, int32_t n_q_heads, const void* k_new
   before_launch(st);
   kv_append_kernel<<<ap.B, kAppendThreads, 0, st>>>(ap);
   return count_launch(AOH_KERNEL_KV_APPEND, st);
+}
+
+aoh_status aoh_kv_append(const void* q_new, int32_t n_q_heads, const void* k_new, const void* v_new, double theta,
+                         const aoh_kv_cache* kv, const aoh_kv_cache* ring, const int32_t* idom, int32_t n_dom,
+                         int32_t* lengths, void* q_out, void* stream) {
+  return append_tokens(q_new, n_q_heads, k_new, v_new, theta, kv, ring, idom, n_dom, lengths, nullptr, q_out, stream);
+}
+
+aoh_status aoh_kv_append_at(const void* q_new, int32_t n_q_heads, const void* k_new, const void* v_new, double theta,
+                            const aoh_kv_cache* kv, const int32_t* idom, int32_t n_dom, int32_t* lengths,
+                            int32_t* positions, void* q_out, void* stream) {
+  if (!kv) return AOH_ERR_INVALID_ARG;
+  if (kv->batch > 0 && !positions) return AOH_ERR_INVALID_ARG;
+  return append_tokens(q_new, n_q_heads, k_new, v_new, theta, kv, nullptr, idom, n_dom, lengths, positions, q_out,
+                       stream);
 }
 
 }  // extern "C"
@@ -1767,3 +1787,316 @@ extern "C" aoh_status aoh_stream_decode_noalloc(const void* q, int32_t n_q_heads
   if ((s = static_scratch_address(&scratch)) != AOH_OK) return s;
   return aoh_stream_decode(q, n_q_heads, kv, roles, sink, window, scale, out, scratch, kStaticScratchBytes, stream);
 }
+
+// ===================================================================== prefill, shared prefix, accumulate, evict
+namespace {
+
+constexpr int kMaxGridZ = 65535;  // sequences of a call whose grids have one layer per sequence
+
+// checks shared by the calls on a linear cache: descriptor, layout, query heads, batch
+aoh_status check_linear(const aoh_kv_cache* kv, int32_t n_q_heads) {
+  aoh_status s = check_kv(kv);
+  if (s != AOH_OK) return s;
+  if (is_ring(kv)) return AOH_ERR_INVALID_ARG;
+  if ((s = check_heads(kv, n_q_heads)) != AOH_OK) return s;
+  if (n_q_heads / kv->n_kv_heads > kMaxQRows || kv->batch > kMaxGridZ) return AOH_ERR_UNSUPPORTED;
+  return AOH_OK;
+}
+
+// KV heads that the cache stores, in order
+int stored_heads(const aoh_kv_cache* kv, uint8_t* out) { return list_heads(kv, nullptr, true, out); }
+
+// Two caches of one call describe the same model heads and store the same ones.
+bool same_heads(const aoh_kv_cache* a, const aoh_kv_cache* b) {
+  if (a->n_kv_heads != b->n_kv_heads || a->head_dim != b->head_dim) return false;
+  for (int g = 0; g < a->n_kv_heads; ++g)
+    if ((slot_of(a, g) == kNoSlot) != (slot_of(b, g) == kNoSlot)) return false;
+  return true;
+}
+
+// Last byte offset + 1 of a cache's K (or V) rows
+uintptr_t rows_extent(const aoh_kv_cache* kv) {
+  int top = 0;
+  for (int g = 0; g < kv->n_kv_heads; ++g)
+    if (slot_of(kv, g) != kNoSlot) top = std::max<int>(top, slot_of(kv, g));
+  return kv->total_tokens > 0
+             ? 2 * (uintptr_t)((kv->total_tokens - 1) * kv->stride_tok + top * kv->stride_head + kv->head_dim)
+             : 0;
+}
+
+bool overlap(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
+// Accumulated-weight decode: the split geometry of a DENSE pass, then the logits
+struct AccumWs {
+  FdGeom geo;
+  int pitch;
+  size_t off_logits, total;
+};
+
+AccumWs accum_ws(const aoh_kv_cache* kv, int32_t Hq) {
+  AccumWs w{};
+  uint8_t roles[kMaxHeads];
+  memset(roles, AOH_ROLE_DENSE, sizeof(roles));
+  w.geo = stream_geom(kv, Hq, roles, 0, 0);
+  w.pitch = (Hq / kv->n_kv_heads + 1) & ~1;
+  w.off_logits = fd_bytes(w.geo);
+  w.total = w.off_logits + align256(sizeof(float) * (size_t)kv->n_kv_heads * (size_t)kv->total_tokens * w.pitch);
+  return w;
+}
+
+template <int D, int NT>
+aoh_status launch_accum_t(AccumParams ap, int max_len, int n_listed, int B, cudaStream_t st) {
+  auto kern = flash_gather_kernel<D, NT, true>;
+  auto merge = accum_merge_kernel<D, NT>;
+  constexpr size_t kMergeSmem = sizeof(float) * 2 * kFdMaxSplits * NT * 8;
+  static std::atomic<uint64_t> configured{0};
+  if (!set_up_on_this_device(configured)) {
+    aoh_status s = set_smem(kern, FdTile<D>::kSmem);
+    if (s == AOH_OK) s = set_smem(merge, kMergeSmem);
+    if (s != AOH_OK) return s;
+    mark_set_up(configured);
+  }
+  FdecParams& fp = ap.fd;
+  aoh_status s = launch_dependent(kern, dim3(fp.max_splits, n_listed, B), fd_threads(NT), FdTile<D>::kSmem, 0, st, fp);
+  if (s != AOH_OK || (s = count_launch(AOH_KERNEL_FLASH_GATHER, st)) != AOH_OK) return s;
+  const int64_t slices = std::max(ceil_div(int64_t(fp.NQ) * (D / 4), kAmOut), ceil_div(std::max(max_len, 1), kAmTokens));
+  s = launch_dependent(merge, dim3((unsigned)slices, n_listed, B), kAmThreads,
+                       sizeof(float) * 2 * (size_t)fp.max_splits * NT * 8, 0, st, ap);
+  return s != AOH_OK ? s : count_launch(AOH_KERNEL_ACCUM_MERGE, st);
+}
+
+// Eviction workspace: the selection's scores, then the select's region
+size_t evict_ws(const aoh_kv_cache* kv, size_t* off_select) {
+  *off_select = align256(sizeof(float) * (size_t)kv->n_kv_heads * (size_t)kv->total_tokens);
+  return *off_select + select_ws(kv).total;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads, int32_t total_q,
+                                         const uint8_t* roles, int32_t sink, int32_t window) {
+  return 0;
+}
+
+aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, const int32_t* q_offsets,
+                              int32_t total_q, const uint8_t* roles, int32_t sink, int32_t window, float scale,
+                              void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  aoh_status s = check_linear(kv, n_q_heads);
+  if (s != AOH_OK) return s;
+  if (!roles) return AOH_ERR_INVALID_ARG;
+  if ((s = check_roles(kv, roles)) != AOH_OK) return s;
+  if (total_q < 0 || sink < 0 || window < 0 || !std::isfinite(scale)) return AOH_ERR_INVALID_ARG;
+  if (kv->batch == 0 || total_q == 0) return AOH_OK;
+  if (!q || !q_offsets || !out) return AOH_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
+  PrefillParams pp{};
+  pp.n_listed = list_heads(kv, roles, false, pp.heads);
+  if (pp.n_listed == 0) return AOH_OK;
+  pp.q = static_cast<const uint16_t*>(q);
+  pp.k = static_cast<const uint16_t*>(kv->k);
+  pp.v = static_cast<const uint16_t*>(kv->v);
+  pp.offsets = kv->offsets;
+  bind_cache(pp, kv);
+  pp.q_offsets = q_offsets;
+  pp.out = static_cast<uint16_t*>(out);
+  pp.stride_tok = kv->stride_tok;
+  pp.stride_head = kv->stride_head;
+  pp.B = kv->batch;
+  pp.Hq = n_q_heads;
+  pp.Hkv = kv->n_kv_heads;
+  pp.G = n_q_heads / kv->n_kv_heads;
+  pp.total_q = total_q;
+  pp.sink = sink;
+  pp.window = window;
+  pp.scale_log2 = scale * 1.4426950408889634f;
+  memcpy(pp.roles, roles, kv->n_kv_heads);
+  cudaStream_t st = as_stream(stream);
+  const int64_t items = int64_t(total_q) * pp.n_listed * pp.G;
+  before_launch(st);
+  if (kv->head_dim == 128)
+    role_prefill_kernel<128><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
+  else
+    role_prefill_kernel<64><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
+  return count_launch(AOH_KERNEL_ROLE_PREFILL, st);
+}
+
+size_t aoh_prefix_decode_workspace_size(const aoh_kv_cache* prefix, const aoh_kv_cache* kv, int32_t n_q_heads) {
+  return 0;
+}
+
+aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache* prefix, const int32_t* seq_start,
+                             const aoh_kv_cache* kv, float scale, float* out, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  aoh_status s = check_linear(prefix, n_q_heads);
+  if (s != AOH_OK || (s = check_linear(kv, n_q_heads)) != AOH_OK) return s;
+  if (!same_heads(prefix, kv)) return AOH_ERR_INVALID_ARG;
+  if (prefix->batch < 1 || (!seq_start && prefix->batch != 1)) return AOH_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return AOH_ERR_INVALID_ARG;
+  if (kv->batch == 0) return AOH_OK;
+  if (!q || !out) return AOH_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
+  PrefixParams pp{};
+  pp.n_listed = stored_heads(kv, pp.heads);
+  if (pp.n_listed == 0) return AOH_OK;
+  pp.q = static_cast<const uint16_t*>(q);
+  pp.pk = static_cast<const uint16_t*>(prefix->k);
+  pp.pv = static_cast<const uint16_t*>(prefix->v);
+  pp.poffsets = prefix->offsets;
+  pp.plengths = prefix->lengths;
+  pp.seq_start = seq_start;
+  pp.pstride_tok = prefix->stride_tok;
+  pp.pstride_head = prefix->stride_head;
+  pp.k = static_cast<const uint16_t*>(kv->k);
+  pp.v = static_cast<const uint16_t*>(kv->v);
+  pp.offsets = kv->offsets;
+  bind_cache(pp, kv);
+  for (int g = 0; g < kv->n_kv_heads; ++g) pp.pslot[g] = slot_of(prefix, g);
+  pp.stride_tok = kv->stride_tok;
+  pp.stride_head = kv->stride_head;
+  pp.out = out;
+  pp.B = kv->batch;
+  pp.NP = prefix->batch;
+  pp.Hq = n_q_heads;
+  pp.Hkv = kv->n_kv_heads;
+  pp.G = n_q_heads / kv->n_kv_heads;
+  pp.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = as_stream(stream);
+  const int64_t items = int64_t(pp.B) * pp.n_listed * pp.G;
+  before_launch(st);
+  if (kv->head_dim == 128)
+    prefix_decode_kernel<128><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
+  else
+    prefix_decode_kernel<64><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
+  return count_launch(AOH_KERNEL_PREFIX_DECODE, st);
+}
+
+size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads) {
+  if (check_linear(kv, n_q_heads) != AOH_OK) return 0;
+  return accum_ws(kv, n_q_heads).total;
+}
+
+aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, float scale, float decay,
+                            const float* mass_in, float* mass_out, float* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  aoh_status s = check_linear(kv, n_q_heads);
+  if (s != AOH_OK) return s;
+  if (!std::isfinite(scale) || !std::isfinite(decay)) return AOH_ERR_INVALID_ARG;
+  if (kv->batch == 0) return AOH_OK;
+  if (!q || !out || (!mass_out && kv->total_tokens > 0)) return AOH_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
+  const AccumWs w = accum_ws(kv, n_q_heads);
+  if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
+  AccumParams ap{};
+  FdecParams& fp = ap.fd;
+  const int n_listed = stored_heads(kv, fp.heads);
+  if (n_listed == 0) return AOH_OK;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  fp.q = static_cast<const uint16_t*>(q);
+  fp.k = static_cast<const uint16_t*>(kv->k);
+  fp.v = static_cast<const uint16_t*>(kv->v);
+  fp.offsets = kv->offsets;
+  bind_cache(fp, kv);
+  fp.out = out;
+  fp.stride_tok = kv->stride_tok;
+  fp.stride_head = kv->stride_head;
+  fp.B = kv->batch;
+  fp.Hq = n_q_heads;
+  fp.Hkv = kv->n_kv_heads;
+  fp.G = fp.NQ = n_q_heads / kv->n_kv_heads;
+  fp.scale_log2 = scale * 1.4426950408889634f;
+  memset(fp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
+  fd_bind(fp, w.geo, ws);
+  fp.keep_partials = 1;
+  fp.logits = reinterpret_cast<float*>(ws + w.off_logits);
+  fp.logit_pitch = w.pitch;
+  fp.T = kv->total_tokens;
+  ap.mass_in = mass_in;
+  ap.mass_out = mass_out;
+  ap.decay = decay;
+  cudaStream_t st = as_stream(stream);
+  if (kv->head_dim == 128) {
+    if (w.geo.nqp == 8) return launch_accum_t<128, 1>(ap, kv->max_len, n_listed, kv->batch, st);
+    if (w.geo.nqp == 16) return launch_accum_t<128, 2>(ap, kv->max_len, n_listed, kv->batch, st);
+    return launch_accum_t<128, 4>(ap, kv->max_len, n_listed, kv->batch, st);
+  }
+  if (w.geo.nqp == 8) return launch_accum_t<64, 1>(ap, kv->max_len, n_listed, kv->batch, st);
+  if (w.geo.nqp == 16) return launch_accum_t<64, 2>(ap, kv->max_len, n_listed, kv->batch, st);
+  return launch_accum_t<64, 4>(ap, kv->max_len, n_listed, kv->batch, st);
+}
+
+size_t aoh_cache_evict_workspace_size(const aoh_kv_cache* src) {
+  size_t o;
+  if (check_linear(src, src ? src->n_kv_heads : 1) != AOH_OK) return 0;
+  return evict_ws(src, &o);
+}
+
+aoh_status aoh_cache_evict(const aoh_kv_cache* src, const float* mass, int32_t budget, int32_t sink, int32_t recent,
+                           const aoh_kv_cache* dst, int32_t* dst_lengths, float* dst_mass, int32_t* idx,
+                           int32_t* count, void* workspace, size_t workspace_bytes, void* stream) {
+  aoh_status s = check_linear(src, src ? src->n_kv_heads : 1);
+  if (s != AOH_OK || (s = check_linear(dst, dst ? dst->n_kv_heads : 1)) != AOH_OK) return s;
+  if (src->batch != dst->batch || !same_heads(src, dst)) return AOH_ERR_INVALID_ARG;
+  if (budget < 1 || sink < 0 || recent < 0 || int64_t(sink) + recent > budget) return AOH_ERR_INVALID_ARG;
+  if (src->batch == 0) return AOH_OK;
+  if (!idx || !count || !dst_lengths || (!mass && src->total_tokens > 0)) return AOH_ERR_INVALID_ARG;
+  const uintptr_t ns = rows_extent(src), nd = rows_extent(dst);
+  if (overlap(src->k, ns, dst->k, nd) || overlap(src->k, ns, dst->v, nd) || overlap(src->v, ns, dst->k, nd) ||
+      overlap(src->v, ns, dst->v, nd))
+    return AOH_ERR_INVALID_ARG;
+  if (dst_mass && overlap(mass, 4 * (uintptr_t)src->total_tokens * src->n_kv_heads, dst_mass,
+                          4 * (uintptr_t)dst->total_tokens * dst->n_kv_heads))
+    return AOH_ERR_INVALID_ARG;
+  if (!select_fits(src)) return AOH_ERR_UNSUPPORTED;
+  size_t off_select;
+  if (!ws_ok(workspace, workspace_bytes, evict_ws(src, &off_select))) return AOH_ERR_WORKSPACE;
+  EvictParams ep{};
+  ep.n_listed = stored_heads(src, ep.heads);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ep.mass = mass;
+  ep.scores = reinterpret_cast<float*>(ws);
+  ep.offsets = src->offsets;
+  bind_cache(ep, src);
+  for (int g = 0; g < dst->n_kv_heads; ++g) ep.dslot[g] = slot_of(dst, g);
+  ep.idx = idx;
+  ep.k = static_cast<const uint16_t*>(src->k);
+  ep.v = static_cast<const uint16_t*>(src->v);
+  ep.stride_tok = src->stride_tok;
+  ep.stride_head = src->stride_head;
+  ep.T = src->total_tokens;
+  ep.dk = static_cast<uint16_t*>(const_cast<void*>(dst->k));
+  ep.dv = static_cast<uint16_t*>(const_cast<void*>(dst->v));
+  ep.doffsets = dst->offsets;
+  ep.dlengths = dst_lengths;
+  ep.dmass = dst_mass;
+  ep.dstride_tok = dst->stride_tok;
+  ep.dstride_head = dst->stride_head;
+  ep.dT = dst->total_tokens;
+  ep.B = src->batch;
+  ep.Hkv = src->n_kv_heads;
+  ep.budget = budget;
+  ep.sink = sink;
+  ep.recent = recent;
+  if (ep.n_listed == 0) return AOH_OK;
+  cudaStream_t st = as_stream(stream);
+  const int chunks = (int)std::max<int64_t>(1, ceil_div(src->max_len, kEvictThreads * 4));
+  if ((s = launch_dependent(evict_key_kernel, dim3(chunks, ep.n_listed, ep.B), kEvictThreads, 0, 0, st, ep)) != AOH_OK ||
+      (s = count_launch(AOH_KERNEL_EVICT_KEY, st)) != AOH_OK)
+    return s;
+  if ((s = launch_select(ep.scores, src, budget, nullptr, budget, idx, count, ep.heads, ep.n_listed, ws + off_select,
+                         st)) != AOH_OK)
+    return s;
+  const int64_t kept = std::max<int64_t>(1, std::min<int64_t>(budget, src->max_len));
+  const dim3 grid((unsigned)ceil_div(kept, kEvictRows), ep.n_listed, ep.B);
+  if (src->head_dim == 128)
+    s = launch_dependent(evict_copy_kernel<128>, grid, kEvictThreads, 0, 0, st, ep);
+  else
+    s = launch_dependent(evict_copy_kernel<64>, grid, kEvictThreads, 0, 0, st, ep);
+  return s != AOH_OK ? s : count_launch(AOH_KERNEL_EVICT_COPY, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,135 @@
+// Eviction from a cache by accumulated attention weight.
+//
+// A row (sequence b, KV head g) of L positions keeps n = min(budget, L) of them: the first
+// `sink`, the last `recent`, and of the others those with the largest accumulated weight
+// mass[g][offsets[b] + p] (equal weights: the lower position).  The kept rows move, in the
+// order of their positions, to the front of the row's region in another cache:
+//     K'[j] = K[idx[j]],  V'[j] = V[idx[j]],  mass'[j] = mass[idx[j]],   j < n,
+// and lengths'[b] = n.  Each KV head keeps positions of its own, all heads equally many.
+//
+//   evict_key_kernel   writes the selection's scores: +inf for the protected positions, else
+//                      the weight, limited to the finite range (a NaN counts as the lightest)
+//                      so that a protected position always comes first;
+//   the exact top-n select of the library on those scores (ascending positions);
+//   evict_copy_kernel  moves the rows.
+// All of it is bound by memory: 4 bytes per (head, position) for the weights and 8 d + 8 per
+// kept row read and written once.
+#pragma once
+
+#include <float.h>
+
+#include "device_common.cuh"
+
+namespace aoh {
+
+struct EvictParams {
+  const float* mass;          // [Hkv][T]
+  float* scores;              // [Hkv][T]
+  const int32_t* offsets;     // [B + 1]
+  const int32_t* lengths;     // [B] or null
+  const int32_t* idx;         // [B][Hkv][budget]
+  // source rows
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t stride_tok, stride_head;
+  int64_t T;
+  // destination
+  uint16_t* dk;
+  uint16_t* dv;
+  const int32_t* doffsets;    // [B + 1]
+  int32_t* dlengths;          // [B]
+  float* dmass;               // [Hkv][dT] or null
+  int64_t dstride_tok, dstride_head;
+  int64_t dT;
+  int32_t B, Hkv, budget, sink, recent;
+  int32_t n_listed;
+  uint8_t heads[kMaxHeads];
+  uint8_t slot[kMaxHeads];    // head slots in the source
+  uint8_t dslot[kMaxHeads];
+};
+
+constexpr int kEvictThreads = 256;
+
+// grid (position chunks of kEvictThreads * 4, listed heads, sequences)
+__global__ void __launch_bounds__(kEvictThreads) evict_key_kernel(const EvictParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int b = blockIdx.z, g = p.heads[blockIdx.y];
+  int off;
+  const int L = seq_length(p.offsets, p.lengths, b, false, &off);
+  const float* src = p.mass + (int64_t)g * p.T + off;
+  float* dst = p.scores + (int64_t)g * p.T + off;
+  const int p0 = blockIdx.x * (kEvictThreads * 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pos = p0 + i * kEvictThreads + threadIdx.x;
+    if (pos < L) {
+      const float m = src[pos];
+      const float lim = m != m ? -INFINITY : fminf(m, FLT_MAX);
+      dst[pos] = (pos < p.sink || pos >= L - p.recent) ? INFINITY : lim;
+    }
+  }
+}
+
+// grid (chunks of kEvictRows kept rows, listed heads, sequences): D / 8 lanes copy one row's 16-byte
+// pieces of K and V; a thread has the loads of all its rows in flight before the first store.
+constexpr int kEvictRows = 64;
+
+template <int D>
+__global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  constexpr int LPR = D / 8;                   // lanes per row
+  constexpr int RPP = kEvictThreads / LPR;     // rows per pass
+  constexpr int NP = kEvictRows / RPP;         // passes
+  const int b = blockIdx.z, g = p.heads[blockIdx.y], tid = threadIdx.x;
+  int off;
+  const int L = seq_length(p.offsets, p.lengths, b, false, &off);
+  const int n = min(L, p.budget);
+  const int doff = p.doffsets[b], dcap = p.doffsets[b + 1] - doff;
+  const bool fits = n <= dcap && doff >= 0 && (int64_t)doff + dcap <= p.dT;
+  if (!fits && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) record_error(kCheckCapacity, b, n, dcap);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.dlengths[b] = fits ? n : 0;
+  if (!fits) return;
+  const int j0 = blockIdx.x * kEvictRows;
+  if (p.dmass) {  // slots past the kept rows start without weight
+    float* dm = p.dmass + (int64_t)g * p.dT + doff;
+    for (int j = n + blockIdx.x * kEvictThreads + tid; j < dcap; j += gridDim.x * kEvictThreads) dm[j] = 0.f;
+  }
+  if (j0 >= n) return;
+  const int32_t* lst = p.idx + ((int64_t)b * p.Hkv + g) * p.budget;
+  const int ch = (tid % LPR) * 8, r0 = tid / LPR;
+  int pos[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int j = j0 + i * RPP + r0;
+    pos[i] = j < n ? lst[j] : -1;
+    if (j < n && (pos[i] < 0 || pos[i] >= L)) {
+      record_error(kCheckPosition, b, g, pos[i]);
+      pos[i] = -1;
+    }
+  }
+  const uint16_t* kb = p.k + (int64_t)off * p.stride_tok + (int64_t)p.slot[g] * p.stride_head + ch;
+  const uint16_t* vb = p.v + (int64_t)off * p.stride_tok + (int64_t)p.slot[g] * p.stride_head + ch;
+  uint4 kr[NP], vr[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    if (pos[i] >= 0) {
+      kr[i] = ld_stream_v4(kb + (int64_t)pos[i] * p.stride_tok);
+      vr[i] = ld_stream_v4(vb + (int64_t)pos[i] * p.stride_tok);
+    }
+  uint16_t* dkb = p.dk + (int64_t)(doff + j0 + r0) * p.dstride_tok + (int64_t)p.dslot[g] * p.dstride_head + ch;
+  uint16_t* dvb = p.dv + (int64_t)(doff + j0 + r0) * p.dstride_tok + (int64_t)p.dslot[g] * p.dstride_head + ch;
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    if (pos[i] >= 0) {
+      *reinterpret_cast<uint4*>(dkb + (int64_t)(i * RPP) * p.dstride_tok) = kr[i];
+      *reinterpret_cast<uint4*>(dvb + (int64_t)(i * RPP) * p.dstride_tok) = vr[i];
+    }
+  if (p.dmass && tid < kEvictRows && j0 + tid < n) {
+    const int s = lst[j0 + tid];
+    if (s >= 0 && s < L) p.dmass[(int64_t)g * p.dT + doff + j0 + tid] = p.mass[(int64_t)g * p.T + off + s];
+  }
+}
+
+}  // namespace aoh

@@ -18,6 +18,9 @@
 //     (token offsets[b] + p of its region) and / or the ring (slot ring_slot(p) of the
 //     ring region; a ring without a window keeps no position past the sink);
 //   * the packed dominant row of every head the linear cache stores, when it has one.
+// With `positions` (a cache whose rows were thinned out by eviction, so that the slot and
+// the position of a token differ) the row still goes to slot lengths[b] but is rotated to
+// positions[b], and both advance by one.
 // A linear region already full, or a ring region smaller than its slots, writes
 // nothing for that sequence and records device check 4.
 #pragma once
@@ -34,6 +37,7 @@ struct AppendParams {
   const uint16_t* v_new;      // [B][Hkv][d]
   uint16_t* q_out;            // [B][Hq][d] rotated, or null
   int32_t* lengths;           // [B]
+  int32_t* positions;         // [B] position to rotate to (advanced by one), or null: lengths[b]
   // linear cache (k null: none)
   uint16_t* k;
   uint16_t* v;
@@ -95,9 +99,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     }
     if (pos < p.ring_sink || p.ring_window > 0) rtok = (int64_t)off + ring_slot(pos, p.ring_sink, p.ring_window);
   }
+  const int rot = p.positions ? p.positions[b] : pos;
+  if (rot < 0 || rot == INT32_MAX) {
+    if (tid == 0) record_error(kCheckCapacity, b, rot, 0);
+    return;
+  }
   if (tid < C) {
     const double w = pow(p.theta, -2.0 * tid / d);
-    sincos((double)pos * w, &s_sin[tid], &s_cos[tid]);
+    sincos((double)rot * w, &s_sin[tid], &s_cos[tid]);
   }
   __syncthreads();
 
@@ -157,7 +166,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     }
   }
   __syncthreads();
-  if (tid == 0) p.lengths[b] = pos + 1;
+  if (tid == 0) {
+    p.lengths[b] = pos + 1;
+    if (p.positions) p.positions[b] = rot + 1;
+  }
 }
 
 }  // namespace aoh

@@ -12,6 +12,10 @@ attends over that index.  By default that is one ``aoh_shared_index_step`` call
 ``fused=False`` makes the three public calls instead (``aoh_tip_score`` with every
 chunk, ``aoh_topk_select``, ``aoh_shared_index_decode``).
 
+``PrefillStep``, ``PrefixDecodeStep``, ``AccumDecodeStep`` and ``EvictStep`` hold the descriptors
+and workspaces of the calls of the same name; ``EvictDecodeStep`` runs decode on a bounded cache
+with them (append, decode with accumulated weights, eviction when the cache is full).
+
 Every call is asynchronous on the current torch stream; nothing is computed in
 Python.
 """
@@ -254,4 +258,165 @@ class OffloadDecodeStep:
     def __call__(self, q: torch.Tensor) -> torch.Tensor:
         B.offload_decode(q, self.oc, self.idom, self.n_dom, self.n_fac, self.n_fac_per_seq, self.n_fac_cap,
                          self.scale, self.out, self.ws, self.idx, self.count)
+        return self.out
+
+
+class PrefillStep:
+    """Attention of new tokens (a prompt, a chunk of one, single tokens) by head role.
+
+    The new tokens' K / V rows are in the cache already: sequence b's n_b query rows are its last
+    n_b positions.  ``q_offsets`` (device int32 [B + 1]) says which rows of q are whose; rows from
+    q_offsets[B] on are left alone.  Output bf16, laid out like q.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, max_len: int, total_tokens: int,
+                 n_q_heads: int, roles: Sequence[int], sink: int, window: int, scale: float, max_total_q: int,
+                 lengths: Optional[torch.Tensor] = None):
+        self.kv = B.make_kv(k, v, offsets, max_len, total_tokens, lengths=lengths)
+        self.roles = B._host_u8(roles)
+        self.sink, self.window, self.scale = int(sink), int(window), float(scale)
+        self.max_total_q = int(max_total_q)
+        self.ws = B.workspace(B.stream_prefill_workspace_size(self.kv, n_q_heads, self.max_total_q, self.roles,
+                                                              self.sink, self.window), k.device)
+
+    def __call__(self, q: torch.Tensor, q_offsets: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if q.shape[0] > self.max_total_q:
+            raise ValueError(f"PrefillStep: {q.shape[0]} query rows, built for {self.max_total_q}")
+        out = torch.zeros_like(q) if out is None else out
+        B.stream_prefill(q, self.kv, q_offsets, self.roles, self.sink, self.window, self.scale, out, self.ws)
+        return out
+
+
+class PrefixDecodeStep:
+    """Decode of a batch whose sequences continue shared prefixes (``aoh_prefix_decode``).
+
+    prefix_k, prefix_v hold the prefixes (prefix i: tokens prefix_offsets[i] ..); sequences
+    [seq_start[i], seq_start[i + 1]) continue prefix i (seq_start None: one prefix, every sequence).
+    k, v hold each sequence's own tokens.
+    """
+
+    def __init__(self, prefix_k: torch.Tensor, prefix_v: torch.Tensor, prefix_offsets: torch.Tensor, prefix_max_len: int,
+                 prefix_tokens: int, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, max_len: int,
+                 total_tokens: int, n_q_heads: int, scale: float, seq_start: Optional[torch.Tensor] = None,
+                 prefix_lengths: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None):
+        self.prefix = B.make_kv(prefix_k, prefix_v, prefix_offsets, prefix_max_len, prefix_tokens,
+                                lengths=prefix_lengths)
+        self.kv = B.make_kv(k, v, offsets, max_len, total_tokens, lengths=lengths)
+        self.seq_start, self.scale = seq_start, float(scale)
+        self.ws = B.workspace(B.prefix_decode_workspace_size(self.prefix, self.kv, n_q_heads), k.device)
+        self.out = torch.zeros((self.kv.batch, n_q_heads, k.shape[2]), dtype=torch.float32, device=k.device)
+
+    def __call__(self, q: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        out = self.out if out is None else out
+        B.prefix_decode(q, self.prefix, self.seq_start, self.kv, self.scale, out, self.ws)
+        return out
+
+
+class AccumDecodeStep:
+    """Decode over the whole cache; mass_out = decay * mass_in + the attention weight of every token.
+
+    mass_in, mass_out: fp32 [Hkv, total_tokens]; mass_in None counts as zeros, and one tensor may be
+    both (mass_out None: in place).
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, max_len: int, total_tokens: int,
+                 n_q_heads: int, scale: float, decay: float = 1.0, lengths: Optional[torch.Tensor] = None):
+        self.kv = B.make_kv(k, v, offsets, max_len, total_tokens, lengths=lengths)
+        self.scale, self.decay = float(scale), float(decay)
+        self.ws = B.workspace(B.accum_decode_workspace_size(self.kv, n_q_heads), k.device)
+        self.out = torch.zeros((self.kv.batch, n_q_heads, k.shape[2]), dtype=torch.float32, device=k.device)
+
+    def __call__(self, q: torch.Tensor, mass_in: Optional[torch.Tensor], mass_out: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        mass_out = mass_in if mass_out is None else mass_out
+        out = self.out if out is None else out
+        B.accum_decode(q, self.kv, self.scale, self.decay, mass_in, mass_out, out, self.ws)
+        return out
+
+
+class EvictStep:
+    """Move the rows that attention has used to another cache (``aoh_cache_evict``).
+
+    Of every sequence's positions each KV head keeps the first ``sink``, the last ``recent`` and the
+    heaviest others, ``budget`` in all.  Returns (idx, count): the kept positions per head.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, max_len: int, total_tokens: int,
+                 dst_k: torch.Tensor, dst_v: torch.Tensor, dst_offsets: torch.Tensor, dst_max_len: int,
+                 dst_total_tokens: int, budget: int, sink: int, recent: int, lengths: Optional[torch.Tensor] = None):
+        self.src = B.make_kv(k, v, offsets, max_len, total_tokens, lengths=lengths)
+        self.dst = B.make_kv(dst_k, dst_v, dst_offsets, dst_max_len, dst_total_tokens)
+        self.budget, self.sink, self.recent = int(budget), int(sink), int(recent)
+        self.idx = torch.empty((self.src.batch, self.src.n_kv_heads, self.budget), dtype=torch.int32, device=k.device)
+        self.count = torch.empty((self.src.batch, self.src.n_kv_heads), dtype=torch.int32, device=k.device)
+        self.ws = B.workspace(B.cache_evict_workspace_size(self.src), k.device)
+
+    def __call__(self, mass: torch.Tensor, dst_mass: Optional[torch.Tensor], dst_lengths: torch.Tensor):
+        B.cache_evict(self.src, mass, self.budget, self.sink, self.recent, self.dst, dst_lengths, dst_mass, self.idx,
+                      self.count, self.ws)
+        return self.idx, self.count
+
+
+class EvictDecodeStep:
+    """Decode with a bounded cache: every sequence holds at most ``budget + slack`` rows per KV head.
+
+    A call appends the new token (rotated to its true position), attends over the cache and adds the
+    attention weights to ``mass``.  When a sequence may be at ``budget + slack`` rows the cache is
+    first thinned to ``budget`` rows per head into the second of two buffers, which then takes its place.  ``load`` fills the
+    cache from a prompt's rows and weights.
+    """
+
+    def __init__(self, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, theta: float, budget: int, slack: int,
+                 sink: int, recent: int, scale: float, decay: float = 1.0, device="cuda"):
+        if slack < 1:
+            raise ValueError("EvictDecodeStep: slack must be at least 1")
+        self.dev = torch.device(device)
+        self.B, self.Hq, self.Hkv, self.d = batch, n_q_heads, n_kv_heads, head_dim
+        self.theta, self.scale, self.decay = float(theta), float(scale), float(decay)
+        self.budget, self.slack, self.sink, self.recent = int(budget), int(slack), int(sink), int(recent)
+        cap = self.cap = self.budget + self.slack
+        T = batch * cap
+        self.offsets = torch.arange(0, T + 1, cap, dtype=torch.int32, device=self.dev)
+        kv_shape = (max(T, 1), n_kv_heads, head_dim)
+        self.k, self.v = ([torch.zeros(kv_shape, dtype=torch.bfloat16, device=self.dev) for _ in range(2)]
+                          for _ in range(2))
+        self.mass_buf = [torch.zeros((n_kv_heads, T), dtype=torch.float32, device=self.dev) for _ in range(2)]
+        self.lengths = [torch.zeros(batch, dtype=torch.int32, device=self.dev) for _ in range(2)]
+        self.positions = torch.zeros(batch, dtype=torch.int32, device=self.dev)
+        self.kv = [B.make_kv(self.k[i], self.v[i], self.offsets, cap, T, lengths=self.lengths[i]) for i in range(2)]
+        self.idx = torch.empty((batch, n_kv_heads, self.budget), dtype=torch.int32, device=self.dev)
+        self.count = torch.empty((batch, n_kv_heads), dtype=torch.int32, device=self.dev)
+        self.ws_accum = B.workspace(B.accum_decode_workspace_size(self.kv[0], n_q_heads), self.dev)
+        self.ws_evict = B.workspace(B.cache_evict_workspace_size(self.kv[0]), self.dev)
+        self.q_rot = torch.zeros((batch, n_q_heads, head_dim), dtype=torch.bfloat16, device=self.dev)
+        self.out = torch.zeros((batch, n_q_heads, head_dim), dtype=torch.float32, device=self.dev)
+        self.cur, self.held = 0, 0  # buffer in use; rows that a sequence holds at most
+
+    @property
+    def mass(self) -> torch.Tensor:
+        return self.mass_buf[self.cur]
+
+    def load(self, src: "B.KVCache", mass: torch.Tensor, positions: torch.Tensor) -> None:
+        """Take the kept rows of a prompt's cache; positions[b] is the next token's position."""
+        ws = B.workspace(B.cache_evict_workspace_size(src), self.dev)
+        B.cache_evict(src, mass, self.budget, self.sink, self.recent, self.kv[self.cur], self.lengths[self.cur],
+                      self.mass_buf[self.cur], self.idx, self.count, ws)
+        self.positions.copy_(positions)
+        self.held = self.budget
+
+    def evict(self) -> None:
+        """Thin the cache to the budget, into the other buffer."""
+        a, b = self.cur, 1 - self.cur
+        B.cache_evict(self.kv[a], self.mass_buf[a], self.budget, self.sink, self.recent, self.kv[b], self.lengths[b],
+                      self.mass_buf[b], self.idx, self.count, self.ws_evict)
+        self.cur, self.held = b, min(self.held, self.budget)
+
+    def __call__(self, q_new: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor) -> torch.Tensor:
+        if self.held == self.cap:
+            self.evict()
+        i = self.cur
+        B.kv_append_at(q_new, k_new, v_new, self.theta, self.kv[i], None, 0, self.lengths[i], self.positions, self.q_rot)
+        B.accum_decode(self.q_rot, self.kv[i], self.scale, self.decay, self.mass_buf[i], self.mass_buf[i], self.out,
+                       self.ws_accum)
+        self.held += 1
         return self.out
