@@ -161,8 +161,8 @@ typedef enum {
   AOH_KERNEL_SELECT_CLUSTER = 14, /* select: one cluster per row, keys on chip      */
   AOH_KERNEL_SELECT_RESOLVE = 15, /* select: exact threshold and chunk offsets per row */
   AOH_KERNEL_FLASH_MERGE = 16,  /* split-K combine of rows with many splits           */
-  AOH_KERNEL_ROLE_PREFILL = 17, /* new tokens attending by head role                  */
-  AOH_KERNEL_PREFIX_DECODE = 18, /* decode over a shared prefix                      */
+  AOH_KERNEL_TILE_ATTEND = 17,  /* tiles of query rows: role prefill, shared prefixes */
+  AOH_KERNEL_TILE_MERGE = 18,   /* join of partial rows of the same                   */
   AOH_KERNEL_ACCUM_MERGE = 19,  /* accumulated weights: combine and weights of a row  */
   AOH_KERNEL_EVICT_KEY = 20,    /* eviction: scores of the selection                 */
   AOH_KERNEL_EVICT_COPY = 21,   /* eviction: kept rows moved to the other cache      */
@@ -201,7 +201,8 @@ void aoh_record_launch_events(void** events, int32_t* kinds, int32_t n);
  * N_fac above the capacity, 3 a chunk id outside [0, d/2), 4 a sequence
  * length or appended position past its region's capacity (or a ring region
  * smaller than its slots), 5 a key Gram matrix without a Cholesky factor
- * (aoh_head_classify: a key block without full row rank).
+ * (aoh_head_classify: a key block without full row rank), 6 a bounded wait inside
+ * a kernel ran out (its outputs are not valid).
  */
 aoh_status aoh_device_check(void* stream, int32_t* detail);
 

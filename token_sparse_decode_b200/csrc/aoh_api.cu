@@ -18,11 +18,10 @@
 #include "head_classify.cuh"
 #include "kv_append.cuh"
 #include "offload.cuh"
-#include "prefix_decode.cuh"
-#include "role_prefill.cuh"
 #include "select_cluster.cuh"
 #include "select_hist.cuh"
 #include "sparse_row.cuh"
+#include "tile_attend.cuh"
 #include "tip_score.cuh"
 
 using namespace aoh;
@@ -1829,6 +1828,210 @@ bool overlap(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
   return na && nb && x < y + nb && y < x + na;
 }
 
+// A gather over every head's whole range that leaves its splits as partials; returns the heads listed.
+int bind_dense(FdecParams& fp, const void* q, int32_t Hq, const aoh_kv_cache* kv, float scale, float* out,
+               const FdGeom& geo, uint8_t* ws) {
+  fp.q = static_cast<const uint16_t*>(q);
+  fp.k = static_cast<const uint16_t*>(kv->k);
+  fp.v = static_cast<const uint16_t*>(kv->v);
+  fp.offsets = kv->offsets;
+  bind_cache(fp, kv);
+  fp.out = out;
+  fp.stride_tok = kv->stride_tok;
+  fp.stride_head = kv->stride_head;
+  fp.B = kv->batch;
+  fp.Hq = Hq;
+  fp.Hkv = kv->n_kv_heads;
+  fp.G = fp.NQ = Hq / kv->n_kv_heads;
+  fp.scale_log2 = scale * 1.4426950408889634f;
+  memset(fp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
+  fd_bind(fp, geo, ws);
+  fp.keep_partials = 1;
+  fp.T = kv->total_tokens;
+  return stored_heads(kv, fp.heads);
+}
+
+template <int D, int NT>
+aoh_status launch_dense_partials_t(const FdecParams& fp, int n_listed, int B, cudaStream_t st) {
+  auto kern = flash_gather_kernel<D, NT, true>;
+  static std::atomic<uint64_t> configured{0};
+  if (!set_up_on_this_device(configured)) {
+    aoh_status s = set_smem(kern, FdTile<D>::kSmem);
+    if (s != AOH_OK) return s;
+    mark_set_up(configured);
+  }
+  aoh_status s = launch_dependent(kern, dim3(fp.max_splits, n_listed, B), fd_threads(NT), FdTile<D>::kSmem, 0, st, fp);
+  return s != AOH_OK ? s : count_launch(AOH_KERNEL_FLASH_GATHER, st);
+}
+
+aoh_status launch_dense_partials(const FdecParams& fp, int d, int nqp, int n_listed, int B, cudaStream_t st) {
+  if (d == 128) {
+    if (nqp == 8) return launch_dense_partials_t<128, 1>(fp, n_listed, B, st);
+    if (nqp == 16) return launch_dense_partials_t<128, 2>(fp, n_listed, B, st);
+    return launch_dense_partials_t<128, 4>(fp, n_listed, B, st);
+  }
+  if (nqp == 8) return launch_dense_partials_t<64, 1>(fp, n_listed, B, st);
+  if (nqp == 16) return launch_dense_partials_t<64, 2>(fp, n_listed, B, st);
+  return launch_dense_partials_t<64, 4>(fp, n_listed, B, st);
+}
+
+FdGeom dense_geom(const aoh_kv_cache* kv, int32_t Hq) {
+  uint8_t roles[kMaxHeads];
+  memset(roles, AOH_ROLE_DENSE, sizeof(roles));
+  return stream_geom(kv, Hq, roles, 0, 0);
+}
+
+// ---- tiles of query rows (role prefill, shared prefixes)
+
+// Listed heads that attend, DENSE ones first: their rows are the longest
+int list_by_role(const aoh_kv_cache* kv, const uint8_t* roles, uint8_t* out) {
+  int n = 0;
+  for (int role : {AOH_ROLE_DENSE, AOH_ROLE_STREAM})
+    for (int g = 0; g < kv->n_kv_heads; ++g)
+      if (roles[g] == role && slot_of(kv, g) != kNoSlot) out[n++] = (uint8_t)g;
+  return n;
+}
+
+struct TileWs {
+  int slots, splits;
+  size_t off_acc, total;
+};
+
+// The grid of a tile call: a slot per two tiles of rows of every group, times the heads, times as
+// many splits of the key range as give every SM a CTA (at least four key tiles each).
+TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, const uint8_t* roles, int32_t sink,
+               int32_t window, int bn, bool keep) {
+  TileWs w{};
+  const int64_t P2 = 2 * (128 / (Hq / kv->n_kv_heads));
+  w.slots = (int)((total_q + groups * (P2 - 1)) / P2);
+  int n_listed = 0;
+  int64_t longest = 0;
+  for (int g = 0; g < kv->n_kv_heads; ++g) {
+    const uint8_t r = roles ? roles[g] : (uint8_t)AOH_ROLE_DENSE;
+    if (r == AOH_ROLE_SPARSE || slot_of(kv, g) == kNoSlot) continue;
+    ++n_listed;
+    const int64_t L = kv->max_len;
+    longest = std::max(longest, r == AOH_ROLE_DENSE ? L : std::min<int64_t>(L, int64_t(sink) + window + P2));
+  }
+  const int64_t ctas = std::max<int64_t>(1, int64_t(w.slots) * n_listed);
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count() / ctas, ceil_div(longest, bn) / 4));
+  if (w.splits > 1 || keep) {
+    const size_t rows = (size_t)w.splits * (size_t)total_q * Hq;
+    w.off_acc = align256(sizeof(float) * 2 * rows);
+    w.total = w.off_acc + align256(sizeof(float) * rows * kv->head_dim);
+  }
+  return w;
+}
+
+// cuTensorMapEncodeTiled through the runtime (the library does not link the driver)
+aoh_status encode_map(CUtensorMap* map, const void* base, uint64_t n1, uint64_t n2, uint64_t stride1, uint64_t stride2,
+                      int d, uint32_t box1, uint32_t box2) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> cached{nullptr};
+  Encode fn = cached.load(std::memory_order_relaxed);
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (!f || res != cudaDriverEntryPointSuccess) return AOH_ERR_UNSUPPORTED;
+    fn = reinterpret_cast<Encode>(f);
+    cached.store(fn, std::memory_order_relaxed);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)d, n1, n2}, strides[2] = {2 * stride1, 2 * stride2};
+  const cuuint32_t box[3] = {64, box1, box2}, ones[3] = {1, 1, 1};
+  // rows outside the tensor read as zeros
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? AOH_OK
+             : AOH_ERR_UNSUPPORTED;
+}
+
+aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_cache* kv, const int32_t* q_offsets,
+                      int64_t total_q, float scale, const TileWs& w, void* workspace, int bn) {
+  const int d = kv->head_dim, G = Hq / kv->n_kv_heads, PT = 128 / G;
+  int slots = 1;
+  for (int g = 0; g < kv->n_kv_heads; ++g)
+    if (slot_of(kv, g) != kNoSlot) slots = std::max(slots, slot_of(kv, g) + 1);
+  const uint64_t T = (uint64_t)std::max<int64_t>(1, kv->total_tokens);
+  aoh_status s = encode_map(&tp.qmap, q, Hq, total_q, d, uint64_t(Hq) * d, d, G, PT);
+  if (s == AOH_OK) s = encode_map(&tp.kmap, kv->k, slots, T, kv->stride_head, kv->stride_tok, d, 1, bn);
+  if (s == AOH_OK) s = encode_map(&tp.vmap, kv->v, slots, T, kv->stride_head, kv->stride_tok, d, 1, bn);
+  if (s != AOH_OK) return s;
+  tp.offsets = kv->offsets;
+  bind_cache(tp, kv);
+  tp.q_offsets = q_offsets;
+  tp.part_ml = static_cast<float*>(workspace);
+  tp.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_acc);
+  tp.B = kv->batch;
+  tp.Hq = Hq;
+  tp.G = G;
+  tp.PT = PT;
+  tp.total_q = (int)total_q;
+  tp.splits = w.splits;
+  // a positive factor: masked scores are -inf before they are scaled, and -inf * 0 is a NaN
+  tp.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);
+  tp.neg = scale < 0.f;
+  return AOH_OK;
+}
+
+template <int D, int PARTS>
+aoh_status launch_tiles(const TileParams& tp, const TileWs& w, int n_listed, cudaStream_t st) {
+  auto kern = tile_attend_kernel<D, PARTS>;
+  constexpr size_t smem = TaTile<D, PARTS>::kSmem;
+  static std::atomic<uint64_t> configured{0};
+  if (!set_up_on_this_device(configured)) {
+    cudaFuncAttributes a;
+    aoh_status s = cuda_status(cudaFuncGetAttributes(&a, kern));
+    if (s != AOH_OK) return s;
+    // the softmax warps' larger register share comes out of what the block is launched with
+    if (a.numRegs < kTaRegsLaunch) return AOH_ERR_UNSUPPORTED;
+    if ((s = set_smem(kern, smem)) != AOH_OK) return s;
+    mark_set_up(configured);
+  }
+  return launch_dependent(kern, dim3(w.slots, n_listed, w.splits), kTaThreads, smem, 0, st, tp);
+}
+
+void bind_merge(MergeParams& mp, const TileParams& tp, int n_listed, void* out) {
+  mp.part_ml = tp.part_ml;
+  mp.part_acc = tp.part_acc;
+  mp.q_offsets = tp.q_offsets;
+  mp.out = out;
+  mp.B = tp.B;
+  mp.Hq = tp.Hq;
+  mp.G = tp.G;
+  mp.total_q = tp.total_q;
+  mp.splits = tp.splits;
+  mp.n_listed = n_listed;
+  memcpy(mp.heads, tp.heads, sizeof(mp.heads));
+}
+
+template <int D, bool BF16>
+aoh_status launch_merge(const MergeParams& mp, cudaStream_t st) {
+  const int64_t blocks = ceil_div(int64_t(mp.total_q) * mp.n_listed * mp.G, kTmThreads / 32);
+  aoh_status s = launch_dependent(tile_merge_kernel<D, BF16>, dim3((unsigned)blocks), kTmThreads, 0, 0, st, mp);
+  return s != AOH_OK ? s : count_launch(AOH_KERNEL_TILE_MERGE, st);
+}
+
+// Shared prefixes: [gather over the sequences' own tokens][tile partials]
+struct PrefixWs {
+  FdGeom own;
+  TileWs tiles;
+  size_t off_tiles, total;
+};
+
+PrefixWs prefix_ws(const aoh_kv_cache* prefix, const aoh_kv_cache* kv, int32_t Hq) {
+  PrefixWs w{};
+  w.own = dense_geom(kv, Hq);
+  w.tiles = tile_ws(prefix, Hq, kv->batch, prefix->batch, nullptr, 0, 0, 64, true);
+  w.off_tiles = fd_bytes(w.own);
+  w.total = w.off_tiles + w.tiles.total;
+  return w;
+}
+
 // Accumulated-weight decode: the split geometry of a DENSE pass, then the logits
 struct AccumWs {
   FdGeom geo;
@@ -1838,9 +2041,7 @@ struct AccumWs {
 
 AccumWs accum_ws(const aoh_kv_cache* kv, int32_t Hq) {
   AccumWs w{};
-  uint8_t roles[kMaxHeads];
-  memset(roles, AOH_ROLE_DENSE, sizeof(roles));
-  w.geo = stream_geom(kv, Hq, roles, 0, 0);
+  w.geo = dense_geom(kv, Hq);
   w.pitch = (Hq / kv->n_kv_heads + 1) & ~1;
   w.off_logits = fd_bytes(w.geo);
   w.total = w.off_logits + align256(sizeof(float) * (size_t)kv->n_kv_heads * (size_t)kv->total_tokens * w.pitch);
@@ -1880,7 +2081,8 @@ extern "C" {
 
 size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads, int32_t total_q,
                                          const uint8_t* roles, int32_t sink, int32_t window) {
-  return 0;
+  if (check_linear(kv, n_q_heads) != AOH_OK || !roles || check_roles(kv, roles) != AOH_OK || total_q < 1) return 0;
+  return tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, 128, false).total;
 }
 
 aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, const int32_t* q_offsets,
@@ -1894,39 +2096,29 @@ aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cac
   if (kv->batch == 0 || total_q == 0) return AOH_OK;
   if (!q || !q_offsets || !out) return AOH_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
-  PrefillParams pp{};
-  pp.n_listed = list_heads(kv, roles, false, pp.heads);
-  if (pp.n_listed == 0) return AOH_OK;
-  pp.q = static_cast<const uint16_t*>(q);
-  pp.k = static_cast<const uint16_t*>(kv->k);
-  pp.v = static_cast<const uint16_t*>(kv->v);
-  pp.offsets = kv->offsets;
-  bind_cache(pp, kv);
-  pp.q_offsets = q_offsets;
-  pp.out = static_cast<uint16_t*>(out);
-  pp.stride_tok = kv->stride_tok;
-  pp.stride_head = kv->stride_head;
-  pp.B = kv->batch;
-  pp.Hq = n_q_heads;
-  pp.Hkv = kv->n_kv_heads;
-  pp.G = n_q_heads / kv->n_kv_heads;
-  pp.total_q = total_q;
-  pp.sink = sink;
-  pp.window = window;
-  pp.scale_log2 = scale * 1.4426950408889634f;
-  memcpy(pp.roles, roles, kv->n_kv_heads);
+  const TileWs w = tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, 128, false);
+  if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
+  TileParams tp{};
+  const int n_listed = list_by_role(kv, roles, tp.heads);
+  if (n_listed == 0) return AOH_OK;
+  if ((s = bind_tiles(tp, q, n_q_heads, kv, q_offsets, total_q, scale, w, workspace, TaTile<128, 1>::BN)) != AOH_OK)
+    return s;
+  tp.out = static_cast<uint16_t*>(out);
+  tp.sink = sink;
+  tp.window = window;
+  tp.causal = 1;
+  memcpy(tp.roles, roles, kv->n_kv_heads);
   cudaStream_t st = as_stream(stream);
-  const int64_t items = int64_t(total_q) * pp.n_listed * pp.G;
-  before_launch(st);
-  if (kv->head_dim == 128)
-    role_prefill_kernel<128><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
-  else
-    role_prefill_kernel<64><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
-  return count_launch(AOH_KERNEL_ROLE_PREFILL, st);
+  s = kv->head_dim == 128 ? launch_tiles<128, 1>(tp, w, n_listed, st) : launch_tiles<64, 1>(tp, w, n_listed, st);
+  if (s != AOH_OK || (s = count_launch(AOH_KERNEL_TILE_ATTEND, st)) != AOH_OK || w.splits == 1) return s;
+  MergeParams mp{};
+  bind_merge(mp, tp, n_listed, out);
+  return kv->head_dim == 128 ? launch_merge<128, true>(mp, st) : launch_merge<64, true>(mp, st);
 }
 
 size_t aoh_prefix_decode_workspace_size(const aoh_kv_cache* prefix, const aoh_kv_cache* kv, int32_t n_q_heads) {
-  return 0;
+  if (check_linear(prefix, n_q_heads) != AOH_OK || check_linear(kv, n_q_heads) != AOH_OK || kv->batch < 1) return 0;
+  return prefix_ws(prefix, kv, n_q_heads).total;
 }
 
 aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache* prefix, const int32_t* seq_start,
@@ -1940,39 +2132,35 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
   if (kv->batch == 0) return AOH_OK;
   if (!q || !out) return AOH_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
-  PrefixParams pp{};
-  pp.n_listed = stored_heads(kv, pp.heads);
-  if (pp.n_listed == 0) return AOH_OK;
-  pp.q = static_cast<const uint16_t*>(q);
-  pp.pk = static_cast<const uint16_t*>(prefix->k);
-  pp.pv = static_cast<const uint16_t*>(prefix->v);
-  pp.poffsets = prefix->offsets;
-  pp.plengths = prefix->lengths;
-  pp.seq_start = seq_start;
-  pp.pstride_tok = prefix->stride_tok;
-  pp.pstride_head = prefix->stride_head;
-  pp.k = static_cast<const uint16_t*>(kv->k);
-  pp.v = static_cast<const uint16_t*>(kv->v);
-  pp.offsets = kv->offsets;
-  bind_cache(pp, kv);
-  for (int g = 0; g < kv->n_kv_heads; ++g) pp.pslot[g] = slot_of(prefix, g);
-  pp.stride_tok = kv->stride_tok;
-  pp.stride_head = kv->stride_head;
-  pp.out = out;
-  pp.B = kv->batch;
-  pp.NP = prefix->batch;
-  pp.Hq = n_q_heads;
-  pp.Hkv = kv->n_kv_heads;
-  pp.G = n_q_heads / kv->n_kv_heads;
-  pp.scale_log2 = scale * 1.4426950408889634f;
+  const PrefixWs w = prefix_ws(prefix, kv, n_q_heads);
+  if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = as_stream(stream);
-  const int64_t items = int64_t(pp.B) * pp.n_listed * pp.G;
-  before_launch(st);
-  if (kv->head_dim == 128)
-    prefix_decode_kernel<128><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
-  else
-    prefix_decode_kernel<64><<<(unsigned)ceil_div(items, 4), 128, 0, st>>>(pp);
-  return count_launch(AOH_KERNEL_PREFIX_DECODE, st);
+  // the sequences' own tokens: split-K gather, every split left as a partial
+  AccumParams ap{};
+  const int n_listed = bind_dense(ap.fd, q, n_q_heads, kv, scale, out, w.own, ws);
+  if (n_listed == 0) return AOH_OK;
+  if ((s = launch_dense_partials(ap.fd, kv->head_dim, w.own.nqp, n_listed, kv->batch, st)) != AOH_OK) return s;
+  // the prefixes: tiles of the sequences' rows
+  TileParams tp{};
+  stored_heads(prefix, tp.heads);
+  if ((s = bind_tiles(tp, q, n_q_heads, prefix, seq_start, kv->batch, scale, w.tiles, ws + w.off_tiles,
+                      TaTile<128, 3>::BN)) != AOH_OK)
+    return s;
+  tp.keep_partials = 1;
+  memset(tp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
+  s = kv->head_dim == 128 ? launch_tiles<128, 3>(tp, w.tiles, n_listed, st) : launch_tiles<64, 3>(tp, w.tiles, n_listed, st);
+  if (s != AOH_OK || (s = count_launch(AOH_KERNEL_TILE_ATTEND, st)) != AOH_OK) return s;
+  MergeParams mp{};
+  bind_merge(mp, tp, n_listed, out);
+  mp.own_ml = ap.fd.part_ml;
+  mp.own_acc = ap.fd.part_acc;
+  mp.offsets = kv->offsets;
+  mp.lengths = kv->lengths;
+  mp.chunk = w.own.chunk;
+  mp.max_splits = w.own.max_splits;
+  mp.nqp = w.own.nqp;
+  return kv->head_dim == 128 ? launch_merge<128, false>(mp, st) : launch_merge<64, false>(mp, st);
 }
 
 size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads) {
@@ -1993,25 +2181,9 @@ aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache
   if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
   AccumParams ap{};
   FdecParams& fp = ap.fd;
-  const int n_listed = stored_heads(kv, fp.heads);
-  if (n_listed == 0) return AOH_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  fp.q = static_cast<const uint16_t*>(q);
-  fp.k = static_cast<const uint16_t*>(kv->k);
-  fp.v = static_cast<const uint16_t*>(kv->v);
-  fp.offsets = kv->offsets;
-  bind_cache(fp, kv);
-  fp.out = out;
-  fp.stride_tok = kv->stride_tok;
-  fp.stride_head = kv->stride_head;
-  fp.B = kv->batch;
-  fp.Hq = n_q_heads;
-  fp.Hkv = kv->n_kv_heads;
-  fp.G = fp.NQ = n_q_heads / kv->n_kv_heads;
-  fp.scale_log2 = scale * 1.4426950408889634f;
-  memset(fp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
-  fd_bind(fp, w.geo, ws);
-  fp.keep_partials = 1;
+  const int n_listed = bind_dense(fp, q, n_q_heads, kv, scale, out, w.geo, ws);
+  if (n_listed == 0) return AOH_OK;
   fp.logits = reinterpret_cast<float*>(ws + w.off_logits);
   fp.logit_pitch = w.pitch;
   fp.T = kv->total_tokens;

@@ -18,6 +18,7 @@ enum DeviceCheck : int {
   kCheckCount = 2,       // a count or per-sequence N_fac above the row capacity
   kCheckChunk = 3,       // a chunk id outside [0, d/2)
   kCheckCapacity = 4,    // a sequence length (or an appended position) past its region's capacity
+  kCheckStall = 6,       // a bounded wait inside a kernel ran out
 };
 
 constexpr uint8_t kNoSlot = 255;  // head_slot entry of a KV head that a cache does not store

@@ -339,7 +339,8 @@ __device__ __forceinline__ void fd_finish(const FdecParams& p, uint8_t* smem, in
   if (tid == 0) p.tickets[row_id] = 0;
 }
 
-// LOGITS: every scaled logit is also stored (role ranges only; the accumulated-weight decode).
+// LOGITS: every scaled logit is also stored where p.logits is set (DENSE linear ranges; the
+// accumulated-weight decode, and the own tokens of the shared-prefix decode).
 template <int D, int NT, bool LOGITS = false>
 __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const FdecParams p) {
   constexpr int ST = kFdStages;
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const Fdec
     const float x3 = tb < nv ? s4[3] * p.scale_log2 : -INFINITY;
     if (LOGITS) {  // a DENSE linear range: list entry j is position j
       const int qc = nt * 8 + 2 * (lane & 3);
-      if (qc < p.logit_pitch) {
+      if (p.logits && qc < p.logit_pitch) {
         float* lg = p.logits + ((int64_t)g * p.T + off + jt) * p.logit_pitch + qc;
         if (ta < nv) *reinterpret_cast<float2*>(lg + (int64_t)ta * p.logit_pitch) = make_float2(x0, x1);
         if (tb < nv) *reinterpret_cast<float2*>(lg + (int64_t)tb * p.logit_pitch) = make_float2(x2, x3);

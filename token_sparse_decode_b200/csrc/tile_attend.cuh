@@ -1,0 +1,487 @@
+// Attention of tiles of query rows over a range of cached positions, on tcgen05.
+//
+// Serves two operations with one body:
+//   * role prefill: group b is a sequence, its query rows are the sequence's last n_b positions;
+//     the row at p sees  DENSE: t <= p,  STREAM: t <= p and (t < sink or t > p - window);
+//   * shared-prefix decode: group i is a prefix, its query rows are the sequences that continue it,
+//     and every row sees all P_i tokens.
+//
+// Rows.  The G q heads of a KV head read the same K / V rows, so a tile of 128 matrix rows packs
+// PT = 128 / G tokens x G heads (row r: token r / G, head r % G; G = 7 fills 126 of 128).  A CTA
+// owns two such tiles of one group and KV head, and `splits` CTAs share their key range when there
+// are few tiles.
+//
+// Pipeline.  One warp brings Q once and then K and V tiles of BN tokens by TMA (128-byte swizzle)
+// into a ring of ST tiles; one thread issues, for tile t = 0, 1 in turn,
+//     O_t += P_t V_j  (P from TMEM),   S_t = Q_t K_{j+1}^T,
+// so that while the tensor core works for one tile the four warps of the other turn its scores into
+// weights; one thread holds one row, no shuffles.  S_t and P_t share TMEM columns: MMAs of one
+// thread run in issue order, so P_t has been read when S_t is overwritten.
+//     TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, 256 + D), O_1 behind it.
+//
+// Softmax.  m is a reference value of the row, not always its running maximum: weights are
+// 2^(scale (s - m)) and O, l are rescaled only when the maximum has grown by more than 2^8 over m
+// (weights stay below 2^8, sums far inside fp32), which leaves most tiles without a pass over O.
+//
+// Weights in the product with V: PARTS = 1 rounds them to bf16 (2^-9 relative, of the order of the
+// rounding of a bf16 output); PARTS = 3 keeps 24 bits as three bf16 terms, each multiplied with V,
+// for fp32 outputs.
+#pragma once
+
+#include <cuda.h>
+
+#include "tcgen05.cuh"
+
+namespace aoh {
+
+constexpr int kTaThreads = 384;       // softmax of tile 0, of tile 1, and a warpgroup of load / MMA warps
+constexpr int kTaRegsSoftmax = 216;   // 2 x 128 x 216 + 128 x 72 = 384 x 168 registers
+constexpr int kTaRegsOther = 72;
+constexpr int kTaRegsLaunch = 168;
+constexpr float kTaGrowth = 8.f;      // log2 of the largest weight before a rescale
+
+template <int D, int PARTS>
+struct TaTile {
+  static constexpr int BN = PARTS == 1 ? 128 : 64;  // tokens per K / V tile: P parts and S fit 128 columns
+  static constexpr int kQBytes = 128 * D * 2;
+  static constexpr int kKvBytes = BN * D * 2;
+  static constexpr int kRing = (229 * 1024 - 5 * 1024 - 2 * kQBytes) / kKvBytes;
+  static constexpr int ST = kRing > 10 ? 10 : kRing;
+  static constexpr int kSmem = 1024 + 2 * kQBytes + ST * kKvBytes;
+};
+
+struct alignas(64) TileParams {
+  CUtensorMap qmap, kmap, vmap;
+  const int32_t* offsets;    // [B + 1] of the cache
+  const int32_t* lengths;    // [B] or null
+  const int32_t* q_offsets;  // [B + 1] rows of every group, or null: one group of all rows
+  uint16_t* out;             // splits == 1: bf16 [total_q][Hq][D]
+  float* part_ml;            // else (m, l) [splits][total_q][Hq][2], m times scale_log2
+  float* part_acc;           //      [splits][total_q][Hq][D]
+  int32_t B, Hq, G, PT, total_q, sink, window, splits;
+  int32_t causal;            // 0: every row sees the whole group
+  int32_t keep_partials;     // 1: partials also when splits == 1
+  float scale_log2;          // > 0; a negative scale negates Q in the product
+  uint32_t neg;
+  uint8_t heads[kMaxHeads];
+  uint8_t roles[kMaxHeads];
+  uint8_t slot[kMaxHeads];
+};
+
+// The group and first row of CTA `slot`: group b's tiles of P2 rows take the slots from
+// floor((q_offsets[b] + b (P2 - 1)) / P2) on, room for ceil(n_b / P2) of them.
+__device__ __forceinline__ bool ta_locate(const TileParams& p, int slot, int* b_out, int* i0, int* n_out, int* q0_out) {
+  const int P2 = 2 * p.PT;
+  int b = 0, q0 = 0, q1 = p.total_q, s0 = 0;
+  if (p.q_offsets) {
+    int lo = 0, hi = p.B - 1;
+    auto first = [&](int i) { return (int)(((int64_t)p.q_offsets[i] + (int64_t)i * (P2 - 1)) / P2); };
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first(mid) <= slot) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    q0 = p.q_offsets[b];
+    q1 = p.q_offsets[b + 1];
+    s0 = first(b);
+  }
+  const int n = q1 - q0;
+  const int64_t i = (int64_t)(slot - s0) * P2;
+  *b_out = b;
+  *i0 = (int)i;
+  *n_out = n;
+  *q0_out = q0;
+  return q0 >= 0 && i >= 0 && i < n;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+template <int D, int PARTS>
+__global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid_constant__ TileParams p) {
+  using T = TaTile<D, PARTS>;
+  constexpr int BN = T::BN, ST = T::ST;
+  constexpr uint32_t kO = 256;
+  extern __shared__ uint8_t ta_smem[];
+  __shared__ __align__(8) uint64_t s_bar[2 * ST + 9];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_stop;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  const uint32_t smem = (smem_u32(ta_smem) + 1023u) & ~1023u;
+  const uint32_t q_s = smem, kv_s = smem + 2 * T::kQBytes;
+  const uint32_t bars = smem_u32(s_bar);
+  auto bar_full = [&](int s) { return bars + 8 * s; };
+  auto bar_empty = [&](int s) { return bars + 8 * (ST + s); };
+  auto bar_s = [&](int t) { return bars + 8 * (2 * ST + t); };      // S_t holds new scores
+  auto bar_p = [&](int t) { return bars + 8 * (2 * ST + 2 + t); };  // P_t is written, O_t rescaled
+  auto bar_o = [&](int t) { return bars + 8 * (2 * ST + 4 + t); };  // O_t is complete
+  const uint32_t bar_q = bars + 8 * (2 * ST + 6), bar_fix = bars + 8 * (2 * ST + 7);
+  const uint32_t bar_end = bars + 8 * (2 * ST + 8);
+
+  grid_dep_wait();
+  if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0 && p.q_offsets[p.B] > p.total_q)
+    record_error(kCheckPosition, p.B, p.q_offsets[p.B], p.total_q);  // rows past those of q are skipped
+  int b, i0, n, q0;
+  if (!ta_locate(p, (int)(gridDim.x - 1 - blockIdx.x), &b, &i0, &n, &q0)) return;  // later rows first: the longest
+  if (q0 + i0 >= p.total_q) return;  // (recorded above)
+  const int g = p.heads[blockIdx.y];
+  const bool dense = p.roles[g] == 1;
+  int off;
+  const int L = seq_length(p.offsets, p.lengths, b, false, &off);
+  const int PT = p.PT;
+  const int np = min(min(2 * PT, n - i0), p.total_q - q0 - i0);  // tokens of this CTA
+  const int tiles = np > PT ? 2 : 1;
+  // key tiles that some row sees: [0, a1) and [b0, b1)
+  const int p_lo = p.causal ? max(L - n + i0, -1) : L - 1;
+  const int p_hi = p.causal ? max(L - n + i0 + np - 1, -1) : L - 1;
+  int a1 = 0, b0 = 0;
+  const int b1 = (p_hi + BN) / BN;  // ceil((p_hi + 1) / BN)
+  if (!dense) {
+    a1 = (min(p.sink, p_hi + 1) + BN - 1) / BN;
+    b0 = p.window == 0 ? b1 : max(a1, max(0, p_lo + 1 - p.window) / BN);
+  }
+  const int n_all = a1 + max(0, b1 - b0);
+  const int j_lo = (int)((int64_t)n_all * blockIdx.z / p.splits);
+  const int n_it = (int)((int64_t)n_all * (blockIdx.z + 1) / p.splits) - j_lo;
+  auto key_tile = [&](int j) { return (j_lo + j < a1 ? j_lo + j : b0 + j_lo + j - a1) * BN; };
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(bar_full(s), 1);
+      mbar_init(bar_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar_s(t), 1);
+      mbar_init(bar_p(t), 4);
+      mbar_init(bar_o(t), 1);
+    }
+    mbar_init(bar_q, 1);
+    mbar_init(bar_fix, 1);
+    mbar_init(bar_end, 1);
+    mbar_init_fence();
+    s_stop = 0;
+  }
+  if (warp == 10) tmem_alloc<512>(smem_u32(&s_tmem));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  volatile int* stop = &s_stop;
+
+  if (wg == 2) {
+    regs_dec<kTaRegsOther>();
+    if (warp == 8 && n_it > 0) {  // ---------------------------------------------- loads
+      if (lane == 0) {
+        tma_prefetch_map(&p.kmap);
+        tma_prefetch_map(&p.vmap);
+        mbar_expect_tx(bar_q, tiles * (D / 64) * 128 * PT * p.G);
+        for (int t = 0; t < tiles; ++t)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(q_s + t * T::kQBytes + h * 16384, &p.qmap, h * 64, g * p.G, q0 + i0 + t * PT, bar_q);
+      }
+      const int slot = p.slot[g];
+      int fixes = 0;
+      for (int i = 0; i < 2 * n_it; ++i) {  // K_0, V_0, K_1, V_1, ...
+        const int s = i % ST, t0 = key_tile(i >> 1);
+        if (!warp_wait(bar_empty(s), ((i / ST) & 1) ^ 1, stop)) break;
+        // V rows past the length may hold anything, and a zero weight times a NaN is a NaN: the last
+        // tile's are cleared before the MMA may see it
+        const bool fix = (i & 1) && t0 + BN > L;
+        const uint32_t dst = kv_s + s * T::kKvBytes;
+        const uint32_t bar = fix ? bar_fix : bar_full(s);
+        if (lane == 0) {
+          mbar_expect_tx(bar, T::kKvBytes);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(dst + h * (BN * 128), (i & 1) ? &p.vmap : &p.kmap, h * 64, slot, off + t0, bar);
+        }
+        __syncwarp();
+        if (fix) {
+          const bool ok = warp_wait(bar_fix, fixes & 1, stop);
+          ++fixes;
+          if (!ok) break;
+          const int r0 = L - t0, chunks = (BN - r0) * 8;  // 16-byte pieces of one half
+          for (int e = lane; e < chunks * (D / 64); e += 32) {
+            const uint32_t at = dst + (e / chunks) * (BN * 128) + r0 * 128 + (e % chunks) * 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};\n" ::"r"(at), "r"(0) : "memory");
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_full(s));
+        }
+      }
+    } else if (warp == 9 && lane == 0 && n_it > 0) {  // ---------------------------- matrix products
+      const uint32_t idesc_s = mma_idesc(BN, false) | (p.neg ? kMmaNegA : 0u);
+      constexpr uint32_t idesc_o = mma_idesc(D, true);
+      auto scores = [&](int t, int s) {  // S_t = Q_t K^T
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          mma_ss(tmem + t * 128, smem_desc(q_s + t * T::kQBytes + (ks >> 2) * 16384 + (ks & 3) * 32, 16),
+                 smem_desc(kv_s + s * T::kKvBytes + (ks >> 2) * (BN * 128) + (ks & 3) * 32, 16), idesc_s, ks > 0);
+        mma_commit(bar_s(t));
+      };
+      auto run = [&]() {
+        if (!mbar_wait(bar_q, 0, stop)) return;
+        if (!mbar_wait(bar_full(0), 0, stop)) return;
+        tc_fence_after();
+        for (int t = 0; t < tiles; ++t) scores(t, 0);
+        mma_commit(bar_empty(0));
+        for (int j = 0; j < n_it; ++j) {
+          const int iv = 2 * j + 1, sv = iv % ST, ik = 2 * j + 2, sk = ik % ST;
+          if (!mbar_wait(bar_full(sv), (iv / ST) & 1, stop)) return;
+          if (j + 1 < n_it && !mbar_wait(bar_full(sk), (ik / ST) & 1, stop)) return;
+          for (int t = 0; t < tiles; ++t) {
+            if (!mbar_wait(bar_p(t), j & 1, stop)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < BN / 16; ++ks)
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part)
+                mma_ts(tmem + kO + t * D, tmem + t * 128 + part * (BN / 2) + ks * 8,
+                       smem_desc(kv_s + sv * T::kKvBytes + ks * 2048, BN * 128), idesc_o, j > 0 || ks > 0 || part > 0);
+            if (j + 1 < n_it) scores(t, sk);
+            else mma_commit(bar_o(t));
+          }
+          mma_commit(bar_empty(sv));
+          if (j + 1 < n_it) mma_commit(bar_empty(sk));
+        }
+      };
+      run();
+    }
+  } else {  // ---------------------------------------------------------------------- softmax of tile wg
+    regs_inc<kTaRegsSoftmax>();
+    const int t = wg, r = tid & 127, wr = r & ~31;
+    const int tok = t * PT + r / p.G, hd = g * p.G + r % p.G;
+    const bool valid = r < PT * p.G && tok < np;
+    const bool live = t < tiles && wr < PT * p.G && t * PT + wr / p.G < np;  // some row of the warp exists
+    const int pos = p.causal ? max(L - n + i0 + tok, -1) : L - 1;
+    const int w_tok_hi = min(t * PT + min(wr + 31, PT * p.G - 1) / p.G, np - 1);
+    const int w_lo = p.causal ? max(L - n + i0 + t * PT + wr / p.G, -1) : L - 1;
+    const int w_hi = p.causal ? max(L - n + i0 + w_tok_hi, -1) : L - 1;
+    const float sc = p.scale_log2;
+    const uint64_t sc2 = f2(sc, sc);
+    const uint32_t lanes = tmem + ((uint32_t)(wr & 96) << 16);
+    const uint32_t s_t = lanes + t * 128, o_t = lanes + kO + t * D;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    if (t < tiles) {
+      for (int j = 0; j < n_it; ++j) {
+        if (!(ok = warp_wait(bar_s(t), j & 1, stop))) break;
+        tc_fence_after();
+        const int t0 = key_tile(j);
+        // (a warp without rows leaves P as it is: rows of a product do not mix)
+        const bool none = t0 > w_hi || (!dense && t0 >= p.sink && t0 + BN - 1 <= w_lo - p.window);
+        if (live && none) {
+          uint32_t z[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) z[e] = 0;
+#pragma unroll
+          for (int c = 0; c < PARTS * BN / 2; c += 32) tmem_st32(s_t + c, z);
+          tmem_wait_st();
+        } else if (live) {
+          uint32_t s[BN];
+#pragma unroll
+          for (int c = 0; c < BN; c += 32) tmem_ld32(s + c, s_t + c);
+          tmem_wait_ld();
+          const bool all = t0 + BN - 1 <= w_lo && (dense || t0 <= p.sink - BN || t0 > w_hi - p.window);
+          if (!all) {
+            const int hi = pos - t0, lo = dense ? -1 : pos - p.window - t0, sk = dense ? 0 : p.sink - t0;
+#pragma unroll
+            for (int c = 0; c < BN; ++c)
+              if (c > hi || (c <= lo && c >= sk)) s[c] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < BN; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool grow = (top - m) * sc > kTaGrowth;  // false while nothing has been seen
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? top : m;
+            const float al = grow ? ex2((m - mn) * sc) : 1.f;
+            l *= al;
+            m = mn;
+            if (j > 0) {
+              const uint64_t al2 = f2(al, al);
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, o_t + c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float x, y;
+                  f2_split(f2_mul(f2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), x, y);
+                  o[e] = __float_as_uint(x);
+                  o[e + 1] = __float_as_uint(y);
+                }
+                tmem_st32(o_t + c, o);
+              }
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : -m * sc;
+          const uint64_t ms2 = f2(ms, ms);
+          uint64_t sum = 0;  // (+0, +0)
+#pragma unroll
+          for (int c0 = 0; c0 < BN; c0 += 64) {
+            uint32_t w[PARTS][32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              float x, y;
+              f2_split(f2_fma(f2(__uint_as_float(s[c0 + 2 * e]), __uint_as_float(s[c0 + 2 * e + 1])), sc2, ms2), x, y);
+              x = ex2(x);
+              y = ex2(y);
+              sum = f2_add(sum, f2(x, y));
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part) {
+                const uint32_t v = pack_bf16x2(x, y);
+                w[part][e] = v;
+                x -= bf16lo(v);
+                y -= bf16hi(v);
+              }
+            }
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) tmem_st32(s_t + part * (BN / 2) + c0 / 2, w[part]);
+          }
+          float x, y;
+          f2_split(sum, x, y);
+          l += x + y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_p(t));
+      }
+      if (ok && n_it > 0) ok = warp_wait(bar_o(t), 0, stop);
+      tc_fence_after();
+      if (ok && live) {
+        const int64_t row = (int64_t)(q0 + i0 + tok) * p.Hq + hd;
+        const bool part = p.splits > 1 || p.keep_partials;
+        const int64_t prow = (int64_t)blockIdx.z * p.total_q * p.Hq + row;
+        const float inv = part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+        if (part && valid) {
+          float* ml = p.part_ml + prow * 2;
+          ml[0] = l > 0.f ? m * sc : -INFINITY;
+          ml[1] = l;
+        }
+#pragma unroll
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (n_it > 0) {
+            tmem_ld32(o, o_t + c);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
+          }
+          if (valid && part) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_acc + prow * D + c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (valid) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                w[u] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * u]) * inv, __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (s_stop && warp == 9 && lane == 0) {
+    // a wait ran out: what is in flight must land before shared memory and TMEM are given back
+    record_error(kCheckStall, b, g, (int)blockIdx.z);
+    mma_commit(bar_end);
+    for (int i = 0; i < kWaitLimit && !mbar_try(bar_end, 0); ++i) {
+    }
+    for (int i = 0; i < (1 << 16); ++i) __nanosleep(20);  // TMA copies issued (about a millisecond)
+  }
+  __syncthreads();
+  if (warp == 10) tmem_dealloc<512>(tmem);
+}
+
+// ---------------------------------------------------------------------- joining partial rows
+struct MergeParams {
+  const float* part_ml;      // tile partials [splits][rows][Hq] ...
+  const float* part_acc;
+  const int32_t* q_offsets;  // rows of every group ([B + 1]) or null: one group of all rows
+  void* out;                 // bf16 or fp32 [total_q][Hq][D]
+  int32_t B, Hq, G, total_q, splits, n_listed;
+  // partials of the split-K gather over the rows' own tokens, or null (row b is sequence b)
+  const float* own_ml;       // [b * n_listed + y][max_splits][NQP][2]
+  const float* own_acc;
+  const int32_t* offsets;
+  const int32_t* lengths;
+  int32_t chunk, max_splits, nqp;
+  uint8_t heads[kMaxHeads];
+};
+
+constexpr int kTmThreads = 128;
+
+// One warp per (row, listed q head).  The partials are added in a fixed order.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParams p) {
+  grid_dep_wait();
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t item = (int64_t)blockIdx.x * (kTmThreads / 32) + (threadIdx.x >> 5);
+  const int per_row = p.n_listed * p.G;
+  const int64_t row = item / per_row;
+  const int hl = (int)(item % per_row), y = hl / p.G, h = p.heads[y] * p.G + hl % p.G;
+  if (row >= p.total_q) return;
+  bool tiles = true;
+  if (p.q_offsets) {  // rows that no group holds have no tile partials
+    tiles = row >= p.q_offsets[0] && row < p.q_offsets[p.B];
+    if (!tiles && !p.own_ml) return;
+    if (!tiles && hl == 0 && lane == 0) record_error(kCheckPosition, (int)row, -1, p.B);
+  }
+  const int ns = tiles ? p.splits : 0;
+  int no = 0;
+  if (p.own_ml) {
+    int off;
+    no = (seq_length(p.offsets, p.lengths, (int)row, false, &off) + p.chunk - 1) / p.chunk;
+  }
+  const int64_t rows = (int64_t)p.total_q * p.Hq, tr = row * p.Hq + h;
+  const int64_t orow = ((row * p.n_listed + y) * p.max_splits) * p.nqp + hl % p.G;
+  auto at = [&](int s) { return s < ns ? s * rows + tr : orow + (int64_t)(s - ns) * p.nqp; };
+  const int nt = ns + no;
+  float M = -INFINITY;
+  for (int s = lane; s < nt; s += 32) M = fmaxf(M, (s < ns ? p.part_ml : p.own_ml)[at(s) * 2]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float acc[E], l = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < nt; ++s) {
+    const int64_t i = at(s);
+    const float* ml = (s < ns ? p.part_ml : p.own_ml) + i * 2;
+    const float* a = (s < ns ? p.part_acc : p.own_acc) + i * D + lane * E;
+    const float w = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - M);
+    l += w * ml[1];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = w > 0.f ? fmaf(w, a[e], acc[e]) : acc[e];
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  if (BF16) {
+    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + tr * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  } else {
+    float* o = static_cast<float*>(p.out) + tr * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = acc[e] * inv;
+  }
+}
+
+}  // namespace aoh
