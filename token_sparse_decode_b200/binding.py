@@ -149,6 +149,20 @@ def _stream(stream: Optional[torch.cuda.Stream]) -> Optional[int]:
     return s.cuda_stream or None
 
 
+def _raw_stream(stream: Optional[torch.cuda.Stream], device: int) -> int:
+    """_stream without the stream object (it costs 2 us of a small step's 10); `device` is the current one."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _device(*caches) -> int:
+    """The current device; every cache descriptor's tensors are on it."""
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2  # -2: no tensor can be there
+    for kv in caches:
+        if getattr(kv, "device", dev) != dev:
+            raise ValueError(f"the cache is on cuda:{kv.device}, the current device is cuda:{dev}")
+    return dev
+
+
 def _host_u8(arr) -> Optional[ctypes.Array]:
     if arr is None or isinstance(arr, ctypes.Array):
         return arr
@@ -173,6 +187,7 @@ def make_kv(k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, max_len: in
     slots = None if head_slot is None else (ctypes.c_uint8 * len(head_slot))(*[int(x) for x in head_slot])
     kv._keep = (k, v, offsets, k_dom, lengths, slots)  # raw pointers: keep their owners alive with the descriptor
     kv.k, kv.v, kv.offsets = k.data_ptr(), v.data_ptr(), offsets.data_ptr()
+    kv.device = k.get_device()
     kv.batch = offsets.numel() - 1
     kv.n_kv_heads = n_kv_heads if n_kv_heads is not None else k.shape[1]
     kv.head_dim = k.shape[2]
@@ -371,37 +386,44 @@ def kv_append(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.T
         int(n_dom), _ptr(lengths), _ptr(q_out), _stream(stream)))
 
 
-def _want(fn: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, *shape) -> None:
-    """t is a contiguous tensor of this type and shape on the current device (None entries: any size)."""
-    if t is None or t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or any(
-            n is not None and m != n for m, n in zip(t.shape, shape)):
+def _want(fn: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, dev: int) -> int:
+    """The address of t, a contiguous tensor of this type and shape on the current device."""
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         got = "None" if t is None else f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}"
-        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {shape}, got {got}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+        raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {got}")
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, the current device is cuda:{dev}")
+    return t.data_ptr()
 
 
-def _want_ws(fn: str, ws: Optional[torch.Tensor]) -> None:
-    if ws is None or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device.type != "cuda" or (
-            ws.device.index != torch.cuda.current_device()):
+def _want_q(fn: str, name: str, t: torch.Tensor, rows: Optional[int], d: int, dev: int) -> tuple:
+    """(shape, address) of a query tensor bf16 [rows, Hq, d] (rows None: any number)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != d or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{fn}: {name} must be [{'rows' if rows is None else rows}, Hq, {d}], got {tuple(shape)}")
+    return shape, _want(fn, name, t, torch.bfloat16, shape, dev)
+
+
+def _want_ws(fn: str, ws: Optional[torch.Tensor], dev: int) -> tuple:
+    if ws is None or ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
         raise ValueError(f"{fn}: the workspace must be a contiguous uint8 tensor on the current device")
+    return ws.data_ptr(), ws.numel()
 
 
 def kv_append_at(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor, theta: float, kv: KVCache,
                  idom: Optional[torch.Tensor], n_dom: int, lengths: torch.Tensor, positions: torch.Tensor,
                  q_out: Optional[torch.Tensor], stream=None) -> None:
     """Append every sequence's token at slot lengths[b], rotated to positions[b]; both advance (aoh_kv_append_at)."""
-    fn, d = "aoh_kv_append_at", kv.head_dim
-    _want(fn, "k_new", k_new, torch.bfloat16, kv.batch, kv.n_kv_heads, d)
-    _want(fn, "v_new", v_new, torch.bfloat16, kv.batch, kv.n_kv_heads, d)
-    _want(fn, "lengths", lengths, torch.int32, kv.batch)
-    _want(fn, "positions", positions, torch.int32, kv.batch)
+    fn, d, dev, n = "aoh_kv_append_at", kv.head_dim, _device(kv), kv.batch
+    k_p = _want(fn, "k_new", k_new, torch.bfloat16, (n, kv.n_kv_heads, d), dev)
+    v_p = _want(fn, "v_new", v_new, torch.bfloat16, (n, kv.n_kv_heads, d), dev)
+    len_p, pos_p = _want(fn, "lengths", lengths, torch.int32, (n,), dev), _want(fn, "positions", positions, torch.int32, (n,), dev)
+    hq, q_p, qo_p = 0, None, None
     if q_new is not None:
-        _want(fn, "q_new", q_new, torch.bfloat16, kv.batch, None, d)
-        _want(fn, "q_out", q_out, torch.bfloat16, *q_new.shape)
-    _check(fn, lib().aoh_kv_append_at(
-        _ptr(q_new), 0 if q_new is None else q_new.shape[-2], _ptr(k_new), _ptr(v_new), float(theta),
-        ctypes.byref(kv), _ptr(idom), int(n_dom), _ptr(lengths), _ptr(positions), _ptr(q_out), _stream(stream)))
+        shape, q_p = _want_q(fn, "q_new", q_new, n, d, dev)
+        hq, qo_p = shape[1], _want(fn, "q_out", q_out, torch.bfloat16, shape, dev)
+    _check(fn, lib().aoh_kv_append_at(q_p, hq, k_p, v_p, theta, kv, _ptr(idom), n_dom, len_p, pos_p, qo_p,
+                                      _raw_stream(stream, dev)))
 
 
 def stream_prefill_workspace_size(kv: KVCache, n_q_heads: int, total_q: int, roles, sink: int, window: int) -> int:
@@ -413,17 +435,16 @@ def stream_prefill_workspace_size(kv: KVCache, n_q_heads: int, total_q: int, rol
 def stream_prefill(q: torch.Tensor, kv: KVCache, q_offsets: torch.Tensor, roles, sink: int, window: int, scale: float,
                    out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Attention of each sequence's new tokens by head role (aoh_stream_prefill); q, out bf16 [rows, Hq, d]."""
-    fn = "aoh_stream_prefill"
-    _want(fn, "q", q, torch.bfloat16, None, None, kv.head_dim)
-    _want(fn, "out", out, torch.bfloat16, *q.shape)
-    _want(fn, "q_offsets", q_offsets, torch.int32, kv.batch + 1)
-    _want_ws(fn, ws)
+    fn, dev = "aoh_stream_prefill", _device(kv)
+    shape, q_p = _want_q(fn, "q", q, None, kv.head_dim, dev)
+    out_p = _want(fn, "out", out, torch.bfloat16, shape, dev)
+    qo_p = _want(fn, "q_offsets", q_offsets, torch.int32, (kv.batch + 1,), dev)
+    ws_p, ws_n = _want_ws(fn, ws, dev)
     r = _host_u8(roles)
     if r is not None and len(r) != kv.n_kv_heads:
         raise ValueError(f"{fn}: {len(r)} roles for {kv.n_kv_heads} KV heads")
-    _check(fn, lib().aoh_stream_prefill(
-        q.data_ptr(), q.shape[1], ctypes.byref(kv), q_offsets.data_ptr(), q.shape[0], ctypes.cast(r, ctypes.c_void_p),
-        sink, window, float(scale), out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    _check(fn, lib().aoh_stream_prefill(q_p, shape[1], kv, qo_p, shape[0], r if r is None else ctypes.addressof(r), sink,
+                                        window, scale, out_p, ws_p, ws_n, _raw_stream(stream, dev)))
 
 
 def prefix_decode_workspace_size(prefix: KVCache, kv: KVCache, n_q_heads: int) -> int:
@@ -433,15 +454,13 @@ def prefix_decode_workspace_size(prefix: KVCache, kv: KVCache, n_q_heads: int) -
 def prefix_decode(q: torch.Tensor, prefix: KVCache, seq_start: Optional[torch.Tensor], kv: KVCache, scale: float,
                   out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Decode over a shared prefix and each sequence's own tokens (aoh_prefix_decode)."""
-    fn = "aoh_prefix_decode"
-    _want(fn, "q", q, torch.bfloat16, kv.batch, None, kv.head_dim)
-    _want(fn, "out", out, torch.float32, *q.shape)
-    if seq_start is not None:
-        _want(fn, "seq_start", seq_start, torch.int32, prefix.batch + 1)
-    _want_ws(fn, ws)
-    _check(fn, lib().aoh_prefix_decode(
-        q.data_ptr(), q.shape[1], ctypes.byref(prefix), _ptr(seq_start), ctypes.byref(kv), float(scale),
-        out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    fn, dev = "aoh_prefix_decode", _device(prefix, kv)
+    shape, q_p = _want_q(fn, "q", q, kv.batch, kv.head_dim, dev)
+    out_p = _want(fn, "out", out, torch.float32, shape, dev)
+    ss_p = None if seq_start is None else _want(fn, "seq_start", seq_start, torch.int32, (prefix.batch + 1,), dev)
+    ws_p, ws_n = _want_ws(fn, ws, dev)
+    _check(fn, lib().aoh_prefix_decode(q_p, shape[1], prefix, ss_p, kv, scale, out_p, ws_p, ws_n,
+                                       _raw_stream(stream, dev)))
 
 
 def accum_decode_workspace_size(kv: KVCache, n_q_heads: int) -> int:
@@ -451,16 +470,15 @@ def accum_decode_workspace_size(kv: KVCache, n_q_heads: int) -> int:
 def accum_decode(q: torch.Tensor, kv: KVCache, scale: float, decay: float, mass_in: Optional[torch.Tensor],
                  mass_out: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """Decode over the whole cache; mass_out = decay * mass_in + the group's attention weights (aoh_accum_decode)."""
-    fn = "aoh_accum_decode"
-    _want(fn, "q", q, torch.bfloat16, kv.batch, None, kv.head_dim)
-    _want(fn, "out", out, torch.float32, *q.shape)
-    if mass_in is not None:
-        _want(fn, "mass_in", mass_in, torch.float32, kv.n_kv_heads, kv.total_tokens)
-    _want(fn, "mass_out", mass_out, torch.float32, kv.n_kv_heads, kv.total_tokens)
-    _want_ws(fn, ws)
-    _check(fn, lib().aoh_accum_decode(
-        q.data_ptr(), q.shape[1], ctypes.byref(kv), float(scale), float(decay), _ptr(mass_in), mass_out.data_ptr(),
-        out.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)))
+    fn, dev = "aoh_accum_decode", _device(kv)
+    shape, q_p = _want_q(fn, "q", q, kv.batch, kv.head_dim, dev)
+    out_p = _want(fn, "out", out, torch.float32, shape, dev)
+    ms = (kv.n_kv_heads, kv.total_tokens)
+    mi_p = None if mass_in is None else _want(fn, "mass_in", mass_in, torch.float32, ms, dev)
+    mo_p = mi_p if mass_out is mass_in and mi_p is not None else _want(fn, "mass_out", mass_out, torch.float32, ms, dev)
+    ws_p, ws_n = _want_ws(fn, ws, dev)
+    _check(fn, lib().aoh_accum_decode(q_p, shape[1], kv, scale, decay, mi_p, mo_p, out_p, ws_p, ws_n,
+                                      _raw_stream(stream, dev)))
 
 
 def cache_evict_workspace_size(src: KVCache) -> int:
@@ -471,18 +489,15 @@ def cache_evict(src: KVCache, mass: torch.Tensor, budget: int, sink: int, recent
                 dst_lengths: torch.Tensor, dst_mass: Optional[torch.Tensor], idx: torch.Tensor, count: torch.Tensor,
                 ws: torch.Tensor, stream=None) -> None:
     """Keep the first, the last and the heaviest rows of every head, moved to another cache (aoh_cache_evict)."""
-    fn = "aoh_cache_evict"
-    _want(fn, "mass", mass, torch.float32, src.n_kv_heads, src.total_tokens)
-    _want(fn, "dst_lengths", dst_lengths, torch.int32, src.batch)
-    if dst_mass is not None:
-        _want(fn, "dst_mass", dst_mass, torch.float32, dst.n_kv_heads, dst.total_tokens)
-    _want(fn, "idx", idx, torch.int32, src.batch, src.n_kv_heads, budget)
-    _want(fn, "count", count, torch.int32, src.batch, src.n_kv_heads)
-    _want_ws(fn, ws)
-    _check(fn, lib().aoh_cache_evict(
-        ctypes.byref(src), mass.data_ptr(), int(budget), int(sink), int(recent), ctypes.byref(dst),
-        dst_lengths.data_ptr(), _ptr(dst_mass), idx.data_ptr(), count.data_ptr(), ws.data_ptr(), ws.numel(),
-        _stream(stream)))
+    fn, dev, n, h = "aoh_cache_evict", _device(src, dst), src.batch, src.n_kv_heads
+    m_p = _want(fn, "mass", mass, torch.float32, (h, src.total_tokens), dev)
+    len_p = _want(fn, "dst_lengths", dst_lengths, torch.int32, (n,), dev)
+    dm_p = None if dst_mass is None else _want(fn, "dst_mass", dst_mass, torch.float32, (dst.n_kv_heads, dst.total_tokens), dev)
+    idx_p = _want(fn, "idx", idx, torch.int32, (n, h, budget), dev)
+    count_p = _want(fn, "count", count, torch.int32, (n, h), dev)
+    ws_p, ws_n = _want_ws(fn, ws, dev)
+    _check(fn, lib().aoh_cache_evict(src, m_p, budget, sink, recent, dst, len_p, dm_p, idx_p, count_p, ws_p, ws_n,
+                                     _raw_stream(stream, dev)))
 
 
 def head_classify_workspace_size(d_model: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
