@@ -1979,7 +1979,8 @@ aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_ca
 }
 
 template <int D, int PARTS>
-aoh_status launch_tiles(const TileParams& tp, const TileWs& w, int n_listed, cudaStream_t st) {
+aoh_status launch_tiles(TileParams& tp, const TileWs& w, int n_listed, cudaStream_t st) {
+  tp.n_listed = n_listed;
   auto kern = tile_attend_kernel<D, PARTS>;
   constexpr size_t smem = TaTile<D, PARTS>::kSmem;
   static std::atomic<uint64_t> configured{0};
@@ -1992,7 +1993,7 @@ aoh_status launch_tiles(const TileParams& tp, const TileWs& w, int n_listed, cud
     if ((s = set_smem(kern, smem)) != AOH_OK) return s;
     mark_set_up(configured);
   }
-  return launch_dependent(kern, dim3(w.slots, n_listed, w.splits), kTaThreads, smem, 0, st, tp);
+  return launch_dependent(kern, dim3((unsigned)(int64_t(w.slots) * n_listed), w.splits), kTaThreads, smem, 0, st, tp);
 }
 
 void bind_merge(MergeParams& mp, const TileParams& tp, int n_listed, void* out) {

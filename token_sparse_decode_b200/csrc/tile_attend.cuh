@@ -38,11 +38,14 @@ constexpr int kTaThreads = 384;       // softmax of tile 0, of tile 1, and a war
 constexpr int kTaRegsSoftmax = 216;   // 2 x 128 x 216 + 128 x 72 = 384 x 168 registers
 constexpr int kTaRegsOther = 72;
 constexpr int kTaRegsLaunch = 168;
+constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
 constexpr float kTaGrowth = 8.f;      // log2 of the largest weight before a rescale
 
 template <int D, int PARTS>
 struct TaTile {
   static constexpr int BN = PARTS == 1 ? 128 : 64;  // tokens per K / V tile: P parts and S fit 128 columns
+  static constexpr int CH = BN / 2;                 // tokens of a half: its weights go to the product while the
+                                                    // other half's are computed
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kKvBytes = BN * D * 2;
   static constexpr int kRing = (229 * 1024 - 5 * 1024 - 2 * kQBytes) / kKvBytes;
@@ -58,7 +61,7 @@ struct alignas(64) TileParams {
   uint16_t* out;             // splits == 1: bf16 [total_q][Hq][D]
   float* part_ml;            // else (m, l) [splits][total_q][Hq][2], m times scale_log2
   float* part_acc;           //      [splits][total_q][Hq][D]
-  int32_t B, Hq, G, PT, total_q, sink, window, splits;
+  int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed;
   int32_t causal;            // 0: every row sees the whole group
   int32_t keep_partials;     // 1: partials also when splits == 1
   float scale_log2;          // > 0; a negative scale negates Q in the product
@@ -94,36 +97,64 @@ __device__ __forceinline__ bool ta_locate(const TileParams& p, int slot, int* b_
   return q0 >= 0 && i >= 0 && i < n;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// 2^x of two numbers without the special-function unit, x <= 8: x = i + f with |f| <= 1/2 (i by adding
+// 1.5 * 2^23), 2^f as a cubic, i added to the exponent.  The cubic is 1 at 0 and fitted here to the
+// smallest relative error, 2^-13.3: a twentieth of the rounding of the weight to bf16 that follows.  At
+// and below -127 the sum of the exponents is zero and so is the result.
+constexpr float kEx2C1 = 0.693282902f, kEx2C2 = 0.242210954f, kEx2C3 = 0.0550089292f;
+
+__device__ __forceinline__ void ex2_poly(uint64_t v, float& x, float& y) {
+  f2_split(v, x, y);
+  const uint64_t c = f2(fmaxf(x, -127.f), fmaxf(y, -127.f));
+  const uint64_t i = f2_add(c, f2(12582912.f, 12582912.f));
+  const uint64_t f = f2_add(c, f2_fma(f2_add(i, f2(-12582912.f, -12582912.f)), f2(-1.f, -1.f), 0));
+  uint64_t r = f2_fma(f2(kEx2C3, kEx2C3), f, f2(kEx2C2, kEx2C2));
+  r = f2_fma(r, f, f2(kEx2C1, kEx2C1));
+  r = f2_fma(r, f, f2(1.f, 1.f));
+  float ix, iy;
+  f2_split(i, ix, iy);
+  f2_split(r, x, y);
+  x = __uint_as_float(__float_as_uint(x) + (__float_as_uint(ix) << 23));
+  y = __uint_as_float(__float_as_uint(y) + (__float_as_uint(iy) << 23));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 template <int D, int PARTS>
 __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid_constant__ TileParams p) {
   using T = TaTile<D, PARTS>;
-  constexpr int BN = T::BN, ST = T::ST;
+  constexpr int BN = T::BN, ST = T::ST, CH = T::CH;
   constexpr uint32_t kO = 256;
   extern __shared__ uint8_t ta_smem[];
-  __shared__ __align__(8) uint64_t s_bar[2 * ST + 9];
+  __shared__ __align__(8) uint64_t s_bar[2 * ST + 11];
   __shared__ uint32_t s_tmem;
   __shared__ int s_stop;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), wg = warp >> 2;  // the same register for the whole warp
   const uint32_t smem = (smem_u32(ta_smem) + 1023u) & ~1023u;
   const uint32_t q_s = smem, kv_s = smem + 2 * T::kQBytes;
   const uint32_t bars = smem_u32(s_bar);
   auto bar_full = [&](int s) { return bars + 8 * s; };
   auto bar_empty = [&](int s) { return bars + 8 * (ST + s); };
   auto bar_s = [&](int t) { return bars + 8 * (2 * ST + t); };      // S_t holds new scores
-  auto bar_p = [&](int t) { return bars + 8 * (2 * ST + 2 + t); };  // P_t is written, O_t rescaled
-  auto bar_o = [&](int t) { return bars + 8 * (2 * ST + 4 + t); };  // O_t is complete
-  const uint32_t bar_q = bars + 8 * (2 * ST + 6), bar_fix = bars + 8 * (2 * ST + 7);
-  const uint32_t bar_end = bars + 8 * (2 * ST + 8);
+  auto bar_o = [&](int t) { return bars + 8 * (2 * ST + 2 + t); };  // O_t is complete
+  auto bar_p = [&](int t, int half) { return bars + 8 * (2 * ST + 4 + 2 * t + half); };  // half of P_t is written (O_t rescaled)
+  const uint32_t bar_q = bars + 8 * (2 * ST + 8), bar_fix = bars + 8 * (2 * ST + 9);
+  const uint32_t bar_end = bars + 8 * (2 * ST + 10);
 
   grid_dep_wait();
-  if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y | blockIdx.z) == 0 && p.q_offsets[p.B] > p.total_q)
+  if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y) == 0 && p.q_offsets[p.B] > p.total_q)
     record_error(kCheckPosition, p.B, p.q_offsets[p.B], p.total_q);  // rows past those of q are skipped
   int b, i0, n, q0;
-  if (!ta_locate(p, (int)(gridDim.x - 1 - blockIdx.x), &b, &i0, &n, &q0)) return;  // later rows first: the longest
+  // later rows first, all heads of a tile together: the longest rows start first
+  const int slot_id = (int)((gridDim.x - 1 - blockIdx.x) / p.n_listed), y = (int)(blockIdx.x % p.n_listed);
+  if (!ta_locate(p, slot_id, &b, &i0, &n, &q0)) return;
   if (q0 + i0 >= p.total_q) return;  // (recorded above)
-  const int g = p.heads[blockIdx.y];
+  const int g = p.heads[y];
   const bool dense = p.roles[g] == 1;
   int off;
   const int L = seq_length(p.offsets, p.lengths, b, false, &off);
@@ -140,8 +171,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     b0 = p.window == 0 ? b1 : max(a1, max(0, p_lo + 1 - p.window) / BN);
   }
   const int n_all = a1 + max(0, b1 - b0);
-  const int j_lo = (int)((int64_t)n_all * blockIdx.z / p.splits);
-  const int n_it = (int)((int64_t)n_all * (blockIdx.z + 1) / p.splits) - j_lo;
+  const int j_lo = (int)((int64_t)n_all * blockIdx.y / p.splits);
+  const int n_it = (int)((int64_t)n_all * (blockIdx.y + 1) / p.splits) - j_lo;
   auto key_tile = [&](int j) { return (j_lo + j < a1 ? j_lo + j : b0 + j_lo + j - a1) * BN; };
 
   if (tid == 0) {
@@ -151,7 +182,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar_s(t), 1);
-      mbar_init(bar_p(t), 4);
+      mbar_init(bar_p(t, 0), 4);
+      mbar_init(bar_p(t, 1), 4);
       mbar_init(bar_o(t), 1);
     }
     mbar_init(bar_q, 1);
@@ -208,40 +240,61 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
           if (lane == 0) mbar_arrive(bar_full(s));
         }
       }
-    } else if (warp == 9 && lane == 0 && n_it > 0) {  // ---------------------------- matrix products
+    } else if (warp == 9 && n_it > 0) {  // ----------------------------------------- matrix products
+      // The whole warp walks through the loop and one elected lane issues, so that descriptors stay in
+      // uniform registers (issued from a branch on the lane, 16 products took 1500 to 2400 cycles and
+      // bounded the kernel).  All 512 columns are this block's, so TMEM addresses start at column 0.
       const uint32_t idesc_s = mma_idesc(BN, false) | (p.neg ? kMmaNegA : 0u);
       constexpr uint32_t idesc_o = mma_idesc(D, true);
+      const uint64_t q_d = smem_desc(q_s, 16), k_d = smem_desc(kv_s, 16), v_d = smem_desc(kv_s, BN * 128);
       auto scores = [&](int t, int s) {  // S_t = Q_t K^T
+        const uint64_t a = q_d + (t * T::kQBytes >> 4), c = k_d + (s * T::kKvBytes >> 4);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          mma_ss(tmem + t * 128, smem_desc(q_s + t * T::kQBytes + (ks >> 2) * 16384 + (ks & 3) * 32, 16),
-                 smem_desc(kv_s + s * T::kKvBytes + (ks >> 2) * (BN * 128) + (ks & 3) * 32, 16), idesc_s, ks > 0);
+          mma_ss(t * 128, a + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4), c + (((ks >> 2) * (BN * 128) + (ks & 3) * 32) >> 4),
+                 idesc_s, ks > 0);
         mma_commit(bar_s(t));
       };
       auto run = [&]() {
-        if (!mbar_wait(bar_q, 0, stop)) return;
-        if (!mbar_wait(bar_full(0), 0, stop)) return;
+        if (!warp_wait(bar_q, 0, stop) || !warp_wait(bar_full(0), 0, stop)) return;
         tc_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-        mma_commit(bar_empty(0));
+        if (elect_one()) {
+          for (int t = 0; t < tiles; ++t) scores(t, 0);
+          mma_commit(bar_empty(0));
+        }
+        __syncwarp();
         for (int j = 0; j < n_it; ++j) {
           const int iv = 2 * j + 1, sv = iv % ST, ik = 2 * j + 2, sk = ik % ST;
-          if (!mbar_wait(bar_full(sv), (iv / ST) & 1, stop)) return;
-          if (j + 1 < n_it && !mbar_wait(bar_full(sk), (ik / ST) & 1, stop)) return;
-          for (int t = 0; t < tiles; ++t) {
-            if (!mbar_wait(bar_p(t), j & 1, stop)) return;
-            tc_fence_after();
+          const bool more = j + 1 < n_it;
+          if (!warp_wait(bar_full(sv), (iv / ST) & 1, stop)) return;
+          if (more && !warp_wait(bar_full(sk), (ik / ST) & 1, stop)) return;
+          const uint64_t c = v_d + (sv * T::kKvBytes >> 4);
 #pragma unroll
-            for (int ks = 0; ks < BN / 16; ++ks)
+          for (int t = 0; t < 2; ++t) {
+            if (t == tiles) break;
 #pragma unroll
-              for (int part = 0; part < PARTS; ++part)
-                mma_ts(tmem + kO + t * D, tmem + t * 128 + part * (BN / 2) + ks * 8,
-                       smem_desc(kv_s + sv * T::kKvBytes + ks * 2048, BN * 128), idesc_o, j > 0 || ks > 0 || part > 0);
-            if (j + 1 < n_it) scores(t, sk);
-            else mma_commit(bar_o(t));
+            for (int half = 0; half < 2; ++half) {
+              if (!warp_wait(bar_p(t, half), j & 1, stop)) return;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int ks = half * CH / 16; ks < (half + 1) * CH / 16; ++ks)
+#pragma unroll
+                  for (int part = 0; part < PARTS; ++part)
+                    mma_ts(kO + t * D, t * 128 + part * (BN / 2) + ks * 8, c + (ks * 2048 >> 4), idesc_o,
+                           j > 0 || ks > 0 || part > 0);
+                if (half == 1) {
+                  if (more) scores(t, sk);
+                  else mma_commit(bar_o(t));
+                  if (t + 1 == tiles) {
+                    mma_commit(bar_empty(sv));
+                    if (more) mma_commit(bar_empty(sk));
+                  }
+                }
+              }
+              __syncwarp();
+            }
           }
-          mma_commit(bar_empty(sv));
-          if (j + 1 < n_it) mma_commit(bar_empty(sk));
         }
       };
       run();
@@ -323,14 +376,20 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
           const uint64_t ms2 = f2(ms, ms);
           uint64_t sum = 0;  // (+0, +0)
 #pragma unroll
-          for (int c0 = 0; c0 < BN; c0 += 64) {
-            uint32_t w[PARTS][32];
+          for (int half = 0; half < 2; ++half) {
+            uint32_t w[PARTS][CH / 2];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < CH / 2; ++e) {
+              const int c = half * CH + 2 * e;
+              const uint64_t v2 = f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2);
               float x, y;
-              f2_split(f2_fma(f2(__uint_as_float(s[c0 + 2 * e]), __uint_as_float(s[c0 + 2 * e + 1])), sc2, ms2), x, y);
-              x = ex2(x);
-              y = ex2(y);
+              if (PARTS == 1 && e % kTaPolyOf < kTaPoly) {
+                ex2_poly(v2, x, y);
+              } else {
+                f2_split(v2, x, y);
+                x = ex2(x);
+                y = ex2(y);
+              }
               sum = f2_add(sum, f2(x, y));
 #pragma unroll
               for (int part = 0; part < PARTS; ++part) {
@@ -341,23 +400,30 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
               }
             }
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) tmem_st32(s_t + part * (BN / 2) + c0 / 2, w[part]);
+            for (int part = 0; part < PARTS; ++part) {
+              if (CH == 64) tmem_st32(s_t + part * (BN / 2) + half * 32, w[part]);
+              else tmem_st16(s_t + part * (BN / 2) + half * 16, w[part]);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p(t, half));
           }
           float x, y;
           f2_split(sum, x, y);
           l += x + y;
-          tmem_wait_st();
+          continue;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_p(t));
+        if (lane < 2) mbar_arrive(bar_p(t, lane));
       }
       if (ok && n_it > 0) ok = warp_wait(bar_o(t), 0, stop);
       tc_fence_after();
       if (ok && live) {
         const int64_t row = (int64_t)(q0 + i0 + tok) * p.Hq + hd;
         const bool part = p.splits > 1 || p.keep_partials;
-        const int64_t prow = (int64_t)blockIdx.z * p.total_q * p.Hq + row;
+        const int64_t prow = (int64_t)blockIdx.y * p.total_q * p.Hq + row;
         const float inv = part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
         if (part && valid) {
           float* ml = p.part_ml + prow * 2;
@@ -398,9 +464,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (s_stop && warp == 9 && lane == 0) {
+  if (s_stop && warp == 9 && elect_one()) {
     // a wait ran out: what is in flight must land before shared memory and TMEM are given back
-    record_error(kCheckStall, b, g, (int)blockIdx.z);
+    record_error(kCheckStall, b, g, (int)blockIdx.y);
     mma_commit(bar_end);
     for (int i = 0; i < kWaitLimit && !mbar_try(bar_end, 0); ++i) {
     }
