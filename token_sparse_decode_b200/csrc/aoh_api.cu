@@ -2027,7 +2027,7 @@ struct PrefixWs {
 PrefixWs prefix_ws(const aoh_kv_cache* prefix, const aoh_kv_cache* kv, int32_t Hq) {
   PrefixWs w{};
   w.own = dense_geom(kv, Hq);
-  w.tiles = tile_ws(prefix, Hq, kv->batch, prefix->batch, nullptr, 0, 0, 64, true);
+  w.tiles = tile_ws(prefix, Hq, kv->batch, prefix->batch, nullptr, 0, 0, TaTile<128, 3>::BN, true);
   w.off_tiles = fd_bytes(w.own);
   w.total = w.off_tiles + w.tiles.total;
   return w;
@@ -2083,7 +2083,7 @@ extern "C" {
 size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads, int32_t total_q,
                                          const uint8_t* roles, int32_t sink, int32_t window) {
   if (check_linear(kv, n_q_heads) != AOH_OK || !roles || check_roles(kv, roles) != AOH_OK || total_q < 1) return 0;
-  return tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, 128, false).total;
+  return tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, TaTile<128, 1>::BN, false).total;
 }
 
 aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, const int32_t* q_offsets,
@@ -2097,7 +2097,7 @@ aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cac
   if (kv->batch == 0 || total_q == 0) return AOH_OK;
   if (!q || !q_offsets || !out) return AOH_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
-  const TileWs w = tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, 128, false);
+  const TileWs w = tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, TaTile<128, 1>::BN, false);
   if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
   TileParams tp{};
   const int n_listed = list_by_role(kv, roles, tp.heads);

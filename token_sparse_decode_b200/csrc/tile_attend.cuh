@@ -20,8 +20,9 @@
 //     TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, 256 + D), O_1 behind it.
 //
 // Softmax.  m is a reference value of the row, not always its running maximum: weights are
-// 2^(scale (s - m)) and O, l are rescaled only when the maximum has grown by more than 2^8 over m
-// (weights stay below 2^8, sums far inside fp32), which leaves most tiles without a pass over O.
+// 2^(scale (s - m)), and O and l are rescaled only when the maximum has outgrown m by more than 2^60
+// (fp32 and bf16 weights, O and l have the exponents for that, and their relative rounding does not
+// depend on m), which is as good as never after a row's first tile.
 //
 // Weights in the product with V: PARTS = 1 rounds them to bf16 (2^-9 relative, of the order of the
 // rounding of a bf16 output); PARTS = 3 keeps 24 bits as three bf16 terms, each multiplied with V,
@@ -39,17 +40,17 @@ constexpr int kTaRegsSoftmax = 216;   // 2 x 128 x 216 + 128 x 72 = 384 x 168 re
 constexpr int kTaRegsOther = 72;
 constexpr int kTaRegsLaunch = 168;
 constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
-constexpr float kTaGrowth = 8.f;      // log2 of the largest weight before a rescale
+constexpr float kTaGrowth = 60.f;     // log2 of the largest weight before a rescale
 
 template <int D, int PARTS>
 struct TaTile {
-  static constexpr int BN = PARTS == 1 ? 128 : 64;  // tokens per K / V tile: P parts and S fit 128 columns
-  static constexpr int CH = BN / 2;                 // tokens of a half: its weights go to the product while the
-                                                    // other half's are computed
+  static constexpr int BN = PARTS == 1 ? 128 : 64;  // tokens per K / V tile: 128 columns hold S and the P parts
+  static constexpr int C0 = PARTS == 1 ? 64 : 32;   // tokens whose weights go to the product first, while the
+                                                    // others' are computed
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kKvBytes = BN * D * 2;
   static constexpr int kRing = (229 * 1024 - 5 * 1024 - 2 * kQBytes) / kKvBytes;
-  static constexpr int ST = kRing > 10 ? 10 : kRing;
+  static constexpr int ST = kRing > 12 ? 12 : kRing;
   static constexpr int kSmem = 1024 + 2 * kQBytes + ST * kKvBytes;
 };
 
@@ -127,7 +128,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 template <int D, int PARTS>
 __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid_constant__ TileParams p) {
   using T = TaTile<D, PARTS>;
-  constexpr int BN = T::BN, ST = T::ST, CH = T::CH;
+  constexpr int BN = T::BN, ST = T::ST, C0 = T::C0;
   constexpr uint32_t kO = 256;
   extern __shared__ uint8_t ta_smem[];
   __shared__ __align__(8) uint64_t s_bar[2 * ST + 11];
@@ -140,9 +141,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const uint32_t bars = smem_u32(s_bar);
   auto bar_full = [&](int s) { return bars + 8 * s; };
   auto bar_empty = [&](int s) { return bars + 8 * (ST + s); };
-  auto bar_s = [&](int t) { return bars + 8 * (2 * ST + t); };      // S_t holds new scores
-  auto bar_o = [&](int t) { return bars + 8 * (2 * ST + 2 + t); };  // O_t is complete
-  auto bar_p = [&](int t, int half) { return bars + 8 * (2 * ST + 4 + 2 * t + half); };  // half of P_t is written (O_t rescaled)
+  auto bar_s = [&](int t) { return bars + 8 * (2 * ST + t); };                    // S_t holds new scores
+  auto bar_o = [&](int t) { return bars + 8 * (2 * ST + 2 + t); };                // O_t is complete
+  auto bar_p = [&](int t, int h) { return bars + 8 * (2 * ST + 4 + 2 * t + h); };  // piece h of P_t written (O_t rescaled)
   const uint32_t bar_q = bars + 8 * (2 * ST + 8), bar_fix = bars + 8 * (2 * ST + 9);
   const uint32_t bar_end = bars + 8 * (2 * ST + 10);
 
@@ -159,7 +160,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   int off;
   const int L = seq_length(p.offsets, p.lengths, b, false, &off);
   const int PT = p.PT;
-  const int np = min(min(2 * PT, n - i0), p.total_q - q0 - i0);  // tokens of this CTA
+  // tokens of this CTA (one minimum of a difference: min(min(2 PT, n - i0), total_q - q0 - i0) came out of
+  // nvcc 12.9 without its second term)
+  const int row_end = min(q0 + n, p.total_q), np = min(row_end - (q0 + i0), 2 * PT);
   const int tiles = np > PT ? 2 : 1;
   // key tiles that some row sees: [0, a1) and [b0, b1)
   const int p_lo = p.causal ? max(L - n + i0, -1) : L - 1;
@@ -214,16 +217,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
       int fixes = 0;
       for (int i = 0; i < 2 * n_it; ++i) {  // K_0, V_0, K_1, V_1, ...
         const int s = i % ST, t0 = key_tile(i >> 1);
+        const bool is_v = i & 1;
         if (!warp_wait(bar_empty(s), ((i / ST) & 1) ^ 1, stop)) break;
         // V rows past the length may hold anything, and a zero weight times a NaN is a NaN: the last
         // tile's are cleared before the MMA may see it
-        const bool fix = (i & 1) && t0 + BN > L;
+        const bool fix = is_v && t0 + BN > L;
         const uint32_t dst = kv_s + s * T::kKvBytes;
         const uint32_t bar = fix ? bar_fix : bar_full(s);
         if (lane == 0) {
           mbar_expect_tx(bar, T::kKvBytes);
           for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(dst + h * (BN * 128), (i & 1) ? &p.vmap : &p.kmap, h * 64, slot, off + t0, bar);
+            tma_load_3d(dst + h * (BN * 128), is_v ? &p.vmap : &p.kmap, h * 64, slot, off + t0, bar);
         }
         __syncwarp();
         if (fix) {
@@ -263,27 +267,28 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
           mma_commit(bar_empty(0));
         }
         __syncwarp();
+        int sv = 1, ph = 0;  // stage and phase of V_j; K_{j+1} is in the next one
         for (int j = 0; j < n_it; ++j) {
-          const int iv = 2 * j + 1, sv = iv % ST, ik = 2 * j + 2, sk = ik % ST;
           const bool more = j + 1 < n_it;
-          if (!warp_wait(bar_full(sv), (iv / ST) & 1, stop)) return;
-          if (more && !warp_wait(bar_full(sk), (ik / ST) & 1, stop)) return;
+          const int sk = sv + 1 == ST ? 0 : sv + 1, pk = sv + 1 == ST ? ph ^ 1 : ph;
+          if (!warp_wait(bar_full(sv), ph, stop)) return;
+          if (more && !warp_wait(bar_full(sk), pk, stop)) return;
           const uint64_t c = v_d + (sv * T::kKvBytes >> 4);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             if (t == tiles) break;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!warp_wait(bar_p(t, half), j & 1, stop)) return;
+            for (int h = 0; h < 2; ++h) {
+              if (!warp_wait(bar_p(t, h), j & 1, stop)) return;
               tc_fence_after();
               if (elect_one()) {
 #pragma unroll
-                for (int ks = half * CH / 16; ks < (half + 1) * CH / 16; ++ks)
+                for (int ks = h ? C0 / 16 : 0; ks < (h ? BN : C0) / 16; ++ks)
 #pragma unroll
                   for (int part = 0; part < PARTS; ++part)
                     mma_ts(kO + t * D, t * 128 + part * (BN / 2) + ks * 8, c + (ks * 2048 >> 4), idesc_o,
                            j > 0 || ks > 0 || part > 0);
-                if (half == 1) {
+                if (h == 1) {
                   if (more) scores(t, sk);
                   else mma_commit(bar_o(t));
                   if (t + 1 == tiles) {
@@ -295,6 +300,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
               __syncwarp();
             }
           }
+          ph = sk + 1 == ST ? pk ^ 1 : pk;
+          sv = sk + 1 == ST ? 0 : sk + 1;
         }
       };
       run();
@@ -341,12 +348,48 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
             for (int c = 0; c < BN; ++c)
               if (c > hi || (c <= lo && c >= sk)) s[c] = 0xff800000u;
           }
+          // the first piece's weights with the m at hand, and the tile's maximum beside them: the maximum is
+          // off the path from scores to weights unless m has to change
+          float ms = 0.f;
+          uint64_t sum = 0;
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto weights = [&](auto& w, int c0, int n, bool with_max) {  // of tokens c0 .. c0 + 2 n - 1
+            const uint64_t ms2 = f2(ms, ms);
 #pragma unroll
-          for (int c = 0; c < BN; c += 8)
+            for (int e = 0; e < n; ++e) {
+              const int c = c0 + 2 * e;
+              if (with_max) {
+                mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                if (e < (BN - C0) / 2) mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[C0 + 2 * e]), __uint_as_float(s[C0 + 2 * e + 1]));
+              }
+              const uint64_t v2 = f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2);
+              float x, y;
+              if (PARTS == 1 && e % kTaPolyOf < kTaPoly) {
+                ex2_poly(v2, x, y);
+              } else {
+                f2_split(v2, x, y);
+                x = ex2(x);
+                y = ex2(y);
+              }
+              sum = f2_add(sum, f2(x, y));
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+              for (int part = 0; part < PARTS; ++part) {
+                const uint32_t v = pack_bf16x2(x, y);
+                w[part][e] = v;
+                x -= bf16lo(v);
+                y -= bf16hi(v);
+              }
+            }
+          };
+          auto publish = [&](int h) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_p(t, h));
+          };
+          uint32_t w0[PARTS][C0 / 2];
+          if (m != -INFINITY) ms = -m * sc;
+          weights(w0, 0, C0 / 2, true);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           const bool grow = (top - m) * sc > kTaGrowth;  // false while nothing has been seen
           if (__any_sync(0xffffffffu, grow)) {
@@ -371,44 +414,22 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
                 tmem_st32(o_t + c, o);
               }
             }
+            if (m != -INFINITY) ms = -m * sc;
+            sum = 0;
+            weights(w0, 0, C0 / 2, false);
           }
-          const float ms = m == -INFINITY ? 0.f : -m * sc;
-          const uint64_t ms2 = f2(ms, ms);
-          uint64_t sum = 0;  // (+0, +0)
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t w[PARTS][CH / 2];
+          for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-            for (int e = 0; e < CH / 2; ++e) {
-              const int c = half * CH + 2 * e;
-              const uint64_t v2 = f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2);
-              float x, y;
-              if (PARTS == 1 && e % kTaPolyOf < kTaPoly) {
-                ex2_poly(v2, x, y);
-              } else {
-                f2_split(v2, x, y);
-                x = ex2(x);
-                y = ex2(y);
-              }
-              sum = f2_add(sum, f2(x, y));
+            for (int c = 0; c < C0 / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + c, w0[part] + c);
+          publish(0);
+          uint32_t w1[PARTS][(BN - C0) / 2];
+          weights(w1, C0, (BN - C0) / 2, false);
 #pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
-                const uint32_t v = pack_bf16x2(x, y);
-                w[part][e] = v;
-                x -= bf16lo(v);
-                y -= bf16hi(v);
-              }
-            }
+          for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-              if (CH == 64) tmem_st32(s_t + part * (BN / 2) + half * 32, w[part]);
-              else tmem_st16(s_t + part * (BN / 2) + half * 16, w[part]);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_p(t, half));
-          }
+            for (int c = 0; c < (BN - C0) / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + C0 / 2 + c, w1[part] + c);
+          publish(1);
           float x, y;
           f2_split(sum, x, y);
           l += x + y;
