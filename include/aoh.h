@@ -166,7 +166,9 @@ typedef enum {
   AOH_KERNEL_ACCUM_MERGE = 19,  /* accumulated weights: combine and weights of a row  */
   AOH_KERNEL_EVICT_KEY = 20,    /* eviction: scores of the selection                 */
   AOH_KERNEL_EVICT_COPY = 21,   /* eviction: kept rows moved to the other cache      */
-  AOH_KERNEL_KINDS = 22
+  AOH_KERNEL_DENSE_PASS = 22,   /* one pass over a whole cache (accumulated weights, own tokens) */
+  AOH_KERNEL_DENSE_PLAN = 23,   /* tile counts of more than 1024 sequences for it     */
+  AOH_KERNEL_KINDS = 24
 } aoh_kernel_kind;
 
 /*

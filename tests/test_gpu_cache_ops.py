@@ -473,7 +473,7 @@ def test_steps_launch_the_kernels():
     got = launches_of(lambda: pre(q, i32([0, 1, 2])))
     assert got.pop("tile_attend_kernel") == 1
     acc = AccumDecodeStep(c.k, c.v, c.offsets, c.max_len, c.T, 8, 0.1)
-    assert launches_of(lambda: acc(q, torch.zeros((2, c.T), device="cuda"))) == {"flash_gather_kernel": 1,
+    assert launches_of(lambda: acc(q, torch.zeros((2, c.T), device="cuda"))) == {"dense_pass_kernel": 1,
                                                                                   "accum_merge_kernel": 1}
     d = Cache(183, [128, 128], 2, 128)
     ev = EvictStep(c.k, c.v, c.offsets, c.max_len, c.T, d.k, d.v, d.offsets, 128, d.T, 128, 4, 16)

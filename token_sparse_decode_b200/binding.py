@@ -41,7 +41,7 @@ KERNELS = ("tip_score_kernel", "select_hist_kernel", "sparse_row_kernel", "flash
            "group_roles_kernel", "offload_stage_kernel", "offload_split_kernel", "select_chunk_kernel",
            "select_write_kernel", "select_cluster_kernel",
            "select_resolve_kernel", "flash_merge_kernel", "tile_attend_kernel", "tile_merge_kernel",
-           "accum_merge_kernel", "evict_key_kernel", "evict_copy_kernel")
+           "accum_merge_kernel", "evict_key_kernel", "evict_copy_kernel", "dense_pass_kernel", "dense_plan_kernel")
 
 
 class AohError(RuntimeError):

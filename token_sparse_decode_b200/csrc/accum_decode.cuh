@@ -4,13 +4,13 @@
 //     x_ht = scale q_h . k_t,  w_ht = exp(x_ht - m_h) / l_h,  out_h = sum_t w_ht v_t,
 //     mass_out[g][t] = decay mass_in[g][t] + sum_{h in g} w_ht.
 // The final m_h and l_h are known only when the whole row has been read, so the work is two
-// launches: the split-K gather reads K and V once, leaves (m, l, acc) per split and stores the
-// logits (4 bytes per query row and token, against 4 d for the token's K and V: they stay in L2);
-// accum_merge_kernel combines the splits' outputs and, with the row's m and l, turns the logits
-// into weights and adds them to the mass.  Bound by the K / V bytes of the first launch.
+// launches: dense_pass_kernel reads K and V once and stores the logits (4 bytes per query row and
+// token, against 4 d for the token's K and V: they stay in L2); accum_merge_kernel joins the rows
+// that several CTAs shared and, with each row's m and l, turns the logits into weights and adds
+// them to the mass.  Bound by the K / V bytes of the first launch.
 #pragma once
 
-#include "flash_gather.cuh"
+#include "dense_pass.cuh"
 
 namespace aoh {
 
@@ -20,31 +20,46 @@ constexpr int kAmOut = 16;                    // float4 outputs per CTA
 constexpr int kAmGroups = kAmThreads / kAmOut;
 
 struct AccumParams {
-  FdecParams fd;
-  const float* mass_in;   // [Hkv][T]
+  DenseRows rows;
+  const int32_t* offsets;
+  const int32_t* lengths;
+  const float* logits;    // [Hkv][T][logit_pitch]
+  const float* mass_in;   // [Hkv][T] or null
   float* mass_out;        // [Hkv][T], may be mass_in
+  float* out;             // fp32 [B][Hq][D]
+  int64_t T;
+  int32_t logit_pitch, B, Hq, G, n_listed;
   float decay;
+  uint8_t heads[kMaxHeads];
 };
 
 // grid (max(token chunks, output slices), listed heads, sequences)
 template <int D, int NT>
-__global__ void __launch_bounds__(kAmThreads) accum_merge_kernel(const AccumParams ap) {
+__global__ void __launch_bounds__(kAmThreads) accum_merge_kernel(const AccumParams p) {
   grid_dep_wait();
   constexpr int NQP = NT * 8;
-  const FdecParams& p = ap.fd;
   extern __shared__ __align__(16) uint8_t am_smem[];
   float* sml = reinterpret_cast<float*>(am_smem);  // [nsplit][NQP][2]: (m, l), then (w, l)
   __shared__ float sM[NQP], sInv[NQP], s_part[kAmThreads];
   __shared__ float4 sred[kAmGroups][kAmOut];
   const int tid = threadIdx.x, b = blockIdx.z, y = blockIdx.y, g = p.heads[y];
-  const int row_id = b * gridDim.y + y;
-  int off;
+  int off, c0, c1;
   const int L = seq_length(p.offsets, p.lengths, b, false, &off);
-  const int nsplit = (L + p.chunk - 1) / p.chunk;
-  const int n_out = p.NQ * (D / 4), o0 = blockIdx.x * kAmOut, t0 = blockIdx.x * kAmTokens;
-  if (nsplit == 0 || (o0 >= n_out && t0 >= L)) return;  // no position: the gather wrote zero rows
-  const float* rml = p.part_ml + (int64_t)row_id * p.max_splits * NQP * 2;
-  for (int e = tid; e < nsplit * NQP * 2; e += kAmThreads) sml[e] = __ldcg(rml + e);
+  const int n_out = p.G * (D / 4), o0 = blockIdx.x * kAmOut, t0 = blockIdx.x * kAmTokens;
+  if (!dense_row(p.rows, p.n_listed, p.B, y, b, &c0, &c1)) {  // no position: zero rows
+    if (o0 < n_out && tid < kAmOut && o0 + tid < n_out) {
+      const int o = o0 + tid;
+      *reinterpret_cast<float4*>(p.out + ((int64_t)b * p.Hq + g * p.G + o / (D / 4)) * D + (o % (D / 4)) * 4) =
+          make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  const bool joined = c0 == c1;  // one CTA had the whole row and wrote its output
+  if ((joined || o0 >= n_out) && t0 >= L) return;
+  const int nsplit = c1 - c0 + 1;
+  const float* row_ml = p.rows.row_ml + ((int64_t)y * p.B + b) * NQP * 2;
+  for (int e = tid; e < nsplit * NQP * 2; e += kAmThreads)
+    sml[e] = __ldcg(joined ? row_ml + e : p.rows.part_ml + (int64_t)dense_part(c0, e / (NQP * 2)) * NQP * 2 + e % (NQP * 2));
   __syncthreads();
   // row statistics: M_q = max m, L_q = sum 2^(m - M_q) l, in a fixed order
   constexpr int SP = kAmThreads / NQP;
@@ -77,30 +92,30 @@ __global__ void __launch_bounds__(kAmThreads) accum_merge_kernel(const AccumPara
   // the mass of this CTA's tokens
   if (t0 < L) {
     const int t1 = min(L, t0 + kAmTokens);
-    const float* mi = ap.mass_in ? ap.mass_in + (int64_t)g * p.T + off : nullptr;
-    float* mo = ap.mass_out + (int64_t)g * p.T + off;
+    const float* mi = p.mass_in ? p.mass_in + (int64_t)g * p.T + off : nullptr;
+    float* mo = p.mass_out + (int64_t)g * p.T + off;
     const float* lg = p.logits + ((int64_t)g * p.T + off) * p.logit_pitch;
     for (int t = t0 + tid; t < t1; t += kAmThreads) {
       const float2* row = reinterpret_cast<const float2*>(lg + (int64_t)t * p.logit_pitch);
       float s = 0.f;
-      for (int q = 0; q < p.NQ; q += 2) {
+      for (int q = 0; q < p.G; q += 2) {
         const float2 x = __ldcg(row + (q >> 1));
         s += exp2f(x.x - sM[q]) * sInv[q];
-        if (q + 1 < p.NQ) s += exp2f(x.y - sM[q + 1]) * sInv[q + 1];
+        if (q + 1 < p.G) s += exp2f(x.y - sM[q + 1]) * sInv[q + 1];
       }
-      mo[t] = mi ? fmaf(ap.decay, mi[t], s) : s;
+      mo[t] = mi ? fmaf(p.decay, mi[t], s) : s;
     }
   }
 
   // the outputs: slices of kAmOut float4, kAmGroups threads over the splits of each
-  if (o0 < n_out) {
+  if (o0 < n_out && !joined) {
     const int ol = tid % kAmOut, s0 = tid / kAmOut, o = o0 + ol;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     const int qr = o / (D / 4), dd = (o % (D / 4)) * 4;
     if (o < n_out) {
-      const float* col = p.part_acc + (int64_t)row_id * p.max_splits * NQP * D + (int64_t)qr * D + dd;
       for (int s = s0; s < nsplit; s += kAmGroups) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(col + (int64_t)s * NQP * D));
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(
+            p.rows.part_acc + ((int64_t)dense_part(c0, s) * NQP + qr) * D + dd));
         const float w = sml[(s * NQP + qr) * 2];
         A.x += w * v.x;
         A.y += w * v.y;

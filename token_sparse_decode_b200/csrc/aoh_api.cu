@@ -13,6 +13,7 @@
 #include "aoh.h"
 #include "accum_decode.cuh"
 #include "cache_evict.cuh"
+#include "dense_pass.cuh"
 #include "device_common.cuh"
 #include "flash_gather.cuh"
 #include "head_classify.cuh"
@@ -1828,57 +1829,119 @@ bool overlap(const void* a, uintptr_t na, const void* b, uintptr_t nb) {
   return na && nb && x < y + nb && y < x + na;
 }
 
-// A gather over every head's whole range that leaves its splits as partials; returns the heads listed.
-int bind_dense(FdecParams& fp, const void* q, int32_t Hq, const aoh_kv_cache* kv, float scale, float* out,
-               const FdGeom& geo, uint8_t* ws) {
-  fp.q = static_cast<const uint16_t*>(q);
-  fp.k = static_cast<const uint16_t*>(kv->k);
-  fp.v = static_cast<const uint16_t*>(kv->v);
-  fp.offsets = kv->offsets;
-  bind_cache(fp, kv);
-  fp.out = out;
-  fp.stride_tok = kv->stride_tok;
-  fp.stride_head = kv->stride_head;
-  fp.B = kv->batch;
-  fp.Hq = Hq;
-  fp.Hkv = kv->n_kv_heads;
-  fp.G = fp.NQ = Hq / kv->n_kv_heads;
-  fp.scale_log2 = scale * 1.4426950408889634f;
-  memset(fp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
-  fd_bind(fp, geo, ws);
-  fp.keep_partials = 1;
-  fp.T = kv->total_tokens;
-  return stored_heads(kv, fp.heads);
+// cuTensorMapEncodeTiled through the runtime (the library does not link the driver)
+aoh_status encode_map(CUtensorMap* map, const void* base, uint64_t n1, uint64_t n2, uint64_t stride1, uint64_t stride2,
+                      int d, uint32_t box1, uint32_t box2) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::atomic<Encode> cached{nullptr};
+  Encode fn = cached.load(std::memory_order_relaxed);
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (!f || res != cudaDriverEntryPointSuccess) return AOH_ERR_UNSUPPORTED;
+    fn = reinterpret_cast<Encode>(f);
+    cached.store(fn, std::memory_order_relaxed);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)d, n1, n2}, strides[2] = {2 * stride1, 2 * stride2};
+  const cuuint32_t box[3] = {64, box1, box2}, ones[3] = {1, 1, 1};
+  // rows outside the tensor read as zeros
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? AOH_OK
+             : AOH_ERR_UNSUPPORTED;
+}
+
+aoh_status encode_cache(CUtensorMap* k, CUtensorMap* v, const aoh_kv_cache* kv, int tokens) {
+  int slots = 1;
+  for (int g = 0; g < kv->n_kv_heads; ++g)
+    if (slot_of(kv, g) != kNoSlot) slots = std::max(slots, slot_of(kv, g) + 1);
+  const uint64_t T = (uint64_t)std::max<int64_t>(1, kv->total_tokens);
+  aoh_status s = encode_map(k, kv->k, slots, T, kv->stride_head, kv->stride_tok, kv->head_dim, 1, tokens);
+  return s != AOH_OK ? s : encode_map(v, kv->v, slots, T, kv->stride_head, kv->stride_tok, kv->head_dim, 1, tokens);
+}
+
+// ---- one pass over a whole cache (accumulated weights; the own tokens behind a shared prefix)
+struct DenseWs {
+  int nqp, ctas;
+  size_t off_row, off_ml, off_acc, total;
+};
+
+DenseWs dense_ws(const aoh_kv_cache* kv, int32_t Hq) {
+  DenseWs w{};
+  const int G = Hq / kv->n_kv_heads;
+  w.nqp = G <= 8 ? 8 : (G <= 16 ? 16 : 32);
+  uint8_t heads[kMaxHeads];
+  const int64_t rows = int64_t(kv->batch) * stored_heads(kv, heads);
+  w.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), rows * ceil_div(kv->max_len, kDpTile)));
+  w.off_row = align256(sizeof(int32_t) * ((size_t)kv->batch + 1));
+  w.off_ml = w.off_row + align256(sizeof(float) * 2 * (size_t)rows * w.nqp);
+  w.off_acc = w.off_ml + align256(sizeof(float) * 4 * (size_t)w.ctas * w.nqp);
+  w.total = w.off_acc + align256(sizeof(float) * 2 * (size_t)w.ctas * w.nqp * kv->head_dim);
+  return w;
 }
 
 template <int D, int NT>
-aoh_status launch_dense_partials_t(const FdecParams& fp, int n_listed, int B, cudaStream_t st) {
-  auto kern = flash_gather_kernel<D, NT, true>;
+aoh_status launch_dense_t(const DenseParams& dp, int ctas, cudaStream_t st) {
+  auto kern = dense_pass_kernel<D, NT>;
   static std::atomic<uint64_t> configured{0};
   if (!set_up_on_this_device(configured)) {
-    aoh_status s = set_smem(kern, FdTile<D>::kSmem);
+    aoh_status s = set_smem(kern, DpTile<D>::kSmem);
     if (s != AOH_OK) return s;
     mark_set_up(configured);
   }
-  aoh_status s = launch_dependent(kern, dim3(fp.max_splits, n_listed, B), fd_threads(NT), FdTile<D>::kSmem, 0, st, fp);
-  return s != AOH_OK ? s : count_launch(AOH_KERNEL_FLASH_GATHER, st);
+  aoh_status s = launch_dependent(kern, dim3(ctas), kDpThreads, DpTile<D>::kSmem, 0, st, dp);
+  return s != AOH_OK ? s : count_launch(AOH_KERNEL_DENSE_PASS, st);
 }
 
-aoh_status launch_dense_partials(const FdecParams& fp, int d, int nqp, int n_listed, int B, cudaStream_t st) {
-  if (d == 128) {
-    if (nqp == 8) return launch_dense_partials_t<128, 1>(fp, n_listed, B, st);
-    if (nqp == 16) return launch_dense_partials_t<128, 2>(fp, n_listed, B, st);
-    return launch_dense_partials_t<128, 4>(fp, n_listed, B, st);
+// Launches the pass over every stored head; `rows` says where its results are.
+aoh_status launch_dense(const void* q, int32_t Hq, const aoh_kv_cache* kv, float scale, float* out, bool normalise,
+                        float* logits, int logit_pitch, const DenseWs& w, uint8_t* ws, DenseRows* rows, cudaStream_t st) {
+  DenseParams dp{};
+  aoh_status s = encode_cache(&dp.kmap, &dp.vmap, kv, kDpTile);
+  if (s != AOH_OK) return s;
+  dp.q = static_cast<const uint16_t*>(q);
+  dp.offsets = kv->offsets;
+  bind_cache(dp, kv);
+  dp.n_listed = stored_heads(kv, dp.heads);
+  dp.pre = reinterpret_cast<int32_t*>(ws);
+  dp.row_ml = reinterpret_cast<float*>(ws + w.off_row);
+  dp.part_ml = reinterpret_cast<float*>(ws + w.off_ml);
+  dp.part_acc = reinterpret_cast<float*>(ws + w.off_acc);
+  dp.out = out;
+  dp.logits = logits;
+  dp.logit_pitch = logit_pitch;
+  dp.T = kv->total_tokens;
+  dp.B = kv->batch;
+  dp.Hq = Hq;
+  dp.G = Hq / kv->n_kv_heads;
+  dp.normalise = normalise;
+  dp.scale_log2 = scale * 1.4426950408889634f;
+  dp.planned = kv->batch > kDpSeqs;
+  rows->pre = dp.pre;
+  rows->row_ml = dp.row_ml;
+  rows->part_ml = dp.part_ml;
+  rows->part_acc = dp.part_acc;
+  rows->C = w.ctas;
+  rows->nqp = w.nqp;
+  if (dp.planned) {
+    const PlanParams pp{kv->offsets, kv->lengths, dp.pre, kv->batch};
+    if ((s = launch_dependent(dense_plan_kernel, dim3(1), 1024, 0, 0, st, pp)) != AOH_OK ||
+        (s = count_launch(AOH_KERNEL_DENSE_PLAN, st)) != AOH_OK)
+      return s;
   }
-  if (nqp == 8) return launch_dense_partials_t<64, 1>(fp, n_listed, B, st);
-  if (nqp == 16) return launch_dense_partials_t<64, 2>(fp, n_listed, B, st);
-  return launch_dense_partials_t<64, 4>(fp, n_listed, B, st);
-}
-
-FdGeom dense_geom(const aoh_kv_cache* kv, int32_t Hq) {
-  uint8_t roles[kMaxHeads];
-  memset(roles, AOH_ROLE_DENSE, sizeof(roles));
-  return stream_geom(kv, Hq, roles, 0, 0);
+  if (kv->head_dim == 128) {
+    if (w.nqp == 8) return launch_dense_t<128, 1>(dp, w.ctas, st);
+    if (w.nqp == 16) return launch_dense_t<128, 2>(dp, w.ctas, st);
+    return launch_dense_t<128, 4>(dp, w.ctas, st);
+  }
+  if (w.nqp == 8) return launch_dense_t<64, 1>(dp, w.ctas, st);
+  if (w.nqp == 16) return launch_dense_t<64, 2>(dp, w.ctas, st);
+  return launch_dense_t<64, 4>(dp, w.ctas, st);
 }
 
 // ---- tiles of query rows (role prefill, shared prefixes)
@@ -1923,44 +1986,11 @@ TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, 
   return w;
 }
 
-// cuTensorMapEncodeTiled through the runtime (the library does not link the driver)
-aoh_status encode_map(CUtensorMap* map, const void* base, uint64_t n1, uint64_t n2, uint64_t stride1, uint64_t stride2,
-                      int d, uint32_t box1, uint32_t box2) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static std::atomic<Encode> cached{nullptr};
-  Encode fn = cached.load(std::memory_order_relaxed);
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult res;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &res);
-    if (e != cudaSuccess) return cuda_status(e);
-    if (!f || res != cudaDriverEntryPointSuccess) return AOH_ERR_UNSUPPORTED;
-    fn = reinterpret_cast<Encode>(f);
-    cached.store(fn, std::memory_order_relaxed);
-  }
-  const cuuint64_t dims[3] = {(cuuint64_t)d, n1, n2}, strides[2] = {2 * stride1, 2 * stride2};
-  const cuuint32_t box[3] = {64, box1, box2}, ones[3] = {1, 1, 1};
-  // rows outside the tensor read as zeros
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, ones,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? AOH_OK
-             : AOH_ERR_UNSUPPORTED;
-}
-
 aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_cache* kv, const int32_t* q_offsets,
                       int64_t total_q, float scale, const TileWs& w, void* workspace, int bn) {
   const int d = kv->head_dim, G = Hq / kv->n_kv_heads, PT = 128 / G;
-  int slots = 1;
-  for (int g = 0; g < kv->n_kv_heads; ++g)
-    if (slot_of(kv, g) != kNoSlot) slots = std::max(slots, slot_of(kv, g) + 1);
-  const uint64_t T = (uint64_t)std::max<int64_t>(1, kv->total_tokens);
   aoh_status s = encode_map(&tp.qmap, q, Hq, total_q, d, uint64_t(Hq) * d, d, G, PT);
-  if (s == AOH_OK) s = encode_map(&tp.kmap, kv->k, slots, T, kv->stride_head, kv->stride_tok, d, 1, bn);
-  if (s == AOH_OK) s = encode_map(&tp.vmap, kv->v, slots, T, kv->stride_head, kv->stride_tok, d, 1, bn);
-  if (s != AOH_OK) return s;
+  if (s != AOH_OK || (s = encode_cache(&tp.kmap, &tp.vmap, kv, bn)) != AOH_OK) return s;
   tp.offsets = kv->offsets;
   bind_cache(tp, kv);
   tp.q_offsets = q_offsets;
@@ -2017,56 +2047,49 @@ aoh_status launch_merge(const MergeParams& mp, cudaStream_t st) {
   return s != AOH_OK ? s : count_launch(AOH_KERNEL_TILE_MERGE, st);
 }
 
-// Shared prefixes: [gather over the sequences' own tokens][tile partials]
+// Shared prefixes: [pass over the sequences' own tokens][tile partials]
 struct PrefixWs {
-  FdGeom own;
+  DenseWs own;
   TileWs tiles;
   size_t off_tiles, total;
 };
 
 PrefixWs prefix_ws(const aoh_kv_cache* prefix, const aoh_kv_cache* kv, int32_t Hq) {
   PrefixWs w{};
-  w.own = dense_geom(kv, Hq);
+  w.own = dense_ws(kv, Hq);
   w.tiles = tile_ws(prefix, Hq, kv->batch, prefix->batch, nullptr, 0, 0, TaTile<128, 3>::BN, true);
-  w.off_tiles = fd_bytes(w.own);
+  w.off_tiles = w.own.total;
   w.total = w.off_tiles + w.tiles.total;
   return w;
 }
 
-// Accumulated-weight decode: the split geometry of a DENSE pass, then the logits
+// Accumulated-weight decode: the pass, then the logits
 struct AccumWs {
-  FdGeom geo;
+  DenseWs pass;
   int pitch;
-  size_t off_logits, total;
+  size_t total;
 };
 
 AccumWs accum_ws(const aoh_kv_cache* kv, int32_t Hq) {
   AccumWs w{};
-  w.geo = dense_geom(kv, Hq);
+  w.pass = dense_ws(kv, Hq);
   w.pitch = (Hq / kv->n_kv_heads + 1) & ~1;
-  w.off_logits = fd_bytes(w.geo);
-  w.total = w.off_logits + align256(sizeof(float) * (size_t)kv->n_kv_heads * (size_t)kv->total_tokens * w.pitch);
+  w.total = w.pass.total + align256(sizeof(float) * (size_t)kv->n_kv_heads * (size_t)kv->total_tokens * w.pitch);
   return w;
 }
 
 template <int D, int NT>
-aoh_status launch_accum_t(AccumParams ap, int max_len, int n_listed, int B, cudaStream_t st) {
-  auto kern = flash_gather_kernel<D, NT, true>;
-  auto merge = accum_merge_kernel<D, NT>;
-  constexpr size_t kMergeSmem = sizeof(float) * 2 * kFdMaxSplits * NT * 8;
+aoh_status launch_accum_merge(const AccumParams& ap, int max_len, cudaStream_t st) {
+  auto kern = accum_merge_kernel<D, NT>;
+  const size_t smem = sizeof(float) * 2 * (size_t)ap.rows.C * NT * 8;
   static std::atomic<uint64_t> configured{0};
   if (!set_up_on_this_device(configured)) {
-    aoh_status s = set_smem(kern, FdTile<D>::kSmem);
-    if (s == AOH_OK) s = set_smem(merge, kMergeSmem);
+    aoh_status s = set_smem(kern, std::max<size_t>(smem, sizeof(float) * 2 * (size_t)sm_count() * NT * 8));
     if (s != AOH_OK) return s;
     mark_set_up(configured);
   }
-  FdecParams& fp = ap.fd;
-  aoh_status s = launch_dependent(kern, dim3(fp.max_splits, n_listed, B), fd_threads(NT), FdTile<D>::kSmem, 0, st, fp);
-  if (s != AOH_OK || (s = count_launch(AOH_KERNEL_FLASH_GATHER, st)) != AOH_OK) return s;
-  const int64_t slices = std::max(ceil_div(int64_t(fp.NQ) * (D / 4), kAmOut), ceil_div(std::max(max_len, 1), kAmTokens));
-  s = launch_dependent(merge, dim3((unsigned)slices, n_listed, B), kAmThreads,
-                       sizeof(float) * 2 * (size_t)fp.max_splits * NT * 8, 0, st, ap);
+  const int64_t slices = std::max(ceil_div(int64_t(ap.G) * (D / 4), kAmOut), ceil_div(std::max(max_len, 1), kAmTokens));
+  aoh_status s = launch_dependent(kern, dim3((unsigned)slices, ap.n_listed, ap.B), kAmThreads, smem, 0, st, ap);
   return s != AOH_OK ? s : count_launch(AOH_KERNEL_ACCUM_MERGE, st);
 }
 
@@ -2137,11 +2160,12 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
   if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t st = as_stream(stream);
-  // the sequences' own tokens: split-K gather, every split left as a partial
-  AccumParams ap{};
-  const int n_listed = bind_dense(ap.fd, q, n_q_heads, kv, scale, out, w.own, ws);
+  uint8_t heads[kMaxHeads];
+  const int n_listed = stored_heads(kv, heads);
   if (n_listed == 0) return AOH_OK;
-  if ((s = launch_dense_partials(ap.fd, kv->head_dim, w.own.nqp, n_listed, kv->batch, st)) != AOH_OK) return s;
+  MergeParams mp{};
+  // the sequences' own tokens; what one CTA finishes of them waits in out for the merge
+  if ((s = launch_dense(q, n_q_heads, kv, scale, out, false, nullptr, 0, w.own, ws, &mp.own, st)) != AOH_OK) return s;
   // the prefixes: tiles of the sequences' rows
   TileParams tp{};
   stored_heads(prefix, tp.heads);
@@ -2149,18 +2173,11 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
                       TaTile<128, 3>::BN)) != AOH_OK)
     return s;
   tp.keep_partials = 1;
+  tp.late_wait = 1;
   memset(tp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
   s = kv->head_dim == 128 ? launch_tiles<128, 3>(tp, w.tiles, n_listed, st) : launch_tiles<64, 3>(tp, w.tiles, n_listed, st);
   if (s != AOH_OK || (s = count_launch(AOH_KERNEL_TILE_ATTEND, st)) != AOH_OK) return s;
-  MergeParams mp{};
   bind_merge(mp, tp, n_listed, out);
-  mp.own_ml = ap.fd.part_ml;
-  mp.own_acc = ap.fd.part_acc;
-  mp.offsets = kv->offsets;
-  mp.lengths = kv->lengths;
-  mp.chunk = w.own.chunk;
-  mp.max_splits = w.own.max_splits;
-  mp.nqp = w.own.nqp;
   return kv->head_dim == 128 ? launch_merge<128, false>(mp, st) : launch_merge<64, false>(mp, st);
 }
 
@@ -2181,25 +2198,32 @@ aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache
   const AccumWs w = accum_ws(kv, n_q_heads);
   if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
   AccumParams ap{};
-  FdecParams& fp = ap.fd;
+  ap.n_listed = stored_heads(kv, ap.heads);
+  if (ap.n_listed == 0) return AOH_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const int n_listed = bind_dense(fp, q, n_q_heads, kv, scale, out, w.geo, ws);
-  if (n_listed == 0) return AOH_OK;
-  fp.logits = reinterpret_cast<float*>(ws + w.off_logits);
-  fp.logit_pitch = w.pitch;
-  fp.T = kv->total_tokens;
+  float* logits = reinterpret_cast<float*>(ws + w.pass.total);
+  cudaStream_t st = as_stream(stream);
+  if ((s = launch_dense(q, n_q_heads, kv, scale, out, true, logits, w.pitch, w.pass, ws, &ap.rows, st)) != AOH_OK) return s;
+  ap.offsets = kv->offsets;
+  ap.lengths = kv->lengths;
+  ap.logits = logits;
+  ap.logit_pitch = w.pitch;
   ap.mass_in = mass_in;
   ap.mass_out = mass_out;
   ap.decay = decay;
-  cudaStream_t st = as_stream(stream);
+  ap.out = out;
+  ap.T = kv->total_tokens;
+  ap.B = kv->batch;
+  ap.Hq = n_q_heads;
+  ap.G = n_q_heads / kv->n_kv_heads;
   if (kv->head_dim == 128) {
-    if (w.geo.nqp == 8) return launch_accum_t<128, 1>(ap, kv->max_len, n_listed, kv->batch, st);
-    if (w.geo.nqp == 16) return launch_accum_t<128, 2>(ap, kv->max_len, n_listed, kv->batch, st);
-    return launch_accum_t<128, 4>(ap, kv->max_len, n_listed, kv->batch, st);
+    if (w.pass.nqp == 8) return launch_accum_merge<128, 1>(ap, kv->max_len, st);
+    if (w.pass.nqp == 16) return launch_accum_merge<128, 2>(ap, kv->max_len, st);
+    return launch_accum_merge<128, 4>(ap, kv->max_len, st);
   }
-  if (w.geo.nqp == 8) return launch_accum_t<64, 1>(ap, kv->max_len, n_listed, kv->batch, st);
-  if (w.geo.nqp == 16) return launch_accum_t<64, 2>(ap, kv->max_len, n_listed, kv->batch, st);
-  return launch_accum_t<64, 4>(ap, kv->max_len, n_listed, kv->batch, st);
+  if (w.pass.nqp == 8) return launch_accum_merge<64, 1>(ap, kv->max_len, st);
+  if (w.pass.nqp == 16) return launch_accum_merge<64, 2>(ap, kv->max_len, st);
+  return launch_accum_merge<64, 4>(ap, kv->max_len, st);
 }
 
 size_t aoh_cache_evict_workspace_size(const aoh_kv_cache* src) {

@@ -74,11 +74,6 @@ struct FdecParams {
   int32_t ring_sink, ring_window;  // range mode on a ring cache (> 0 sum): position p is kept in
                                    // slot ring_slot(p); 0, 0: position p is token p of the region
   float scale_log2;          // softmax scale * log2(e)
-  int32_t keep_partials;     // 1: every split leaves its partials, also the only one of a row, and no
-                             //    CTA merges them (a kernel that follows combines them)
-  float* logits;             // kernels with LOGITS: [Hkv][T][logit_pitch], logit * scale_log2 of every
-  int32_t logit_pitch;       //    (token, query row); pitch even, >= NQ
-  int64_t T;                 // tokens of the cache (LOGITS)
   uint8_t heads[kMaxHeads];  // listed KV heads (blockIdx.y)
   uint8_t roles[kMaxHeads];  // role of every KV head (range mode)
   uint8_t slot[kMaxHeads];   // head slot of every KV head in K / V
@@ -217,7 +212,7 @@ __device__ __forceinline__ void fd_finish(const FdecParams& p, uint8_t* smem, in
     cluster.sync();  // peers read this CTA's shared memory until here
     return;
   }
-  const bool single = (nsplit == 1 && !p.keep_partials);
+  const bool single = (nsplit == 1);
   float* pml = p.part_ml + ((int64_t)row_id * p.max_splits + split) * NQP * 2;
   float* pacc = p.part_acc + ((int64_t)row_id * p.max_splits + split) * NQP * D;
   for (int e = tid; e < NQP * D; e += kFdThreads) {
@@ -248,7 +243,7 @@ __device__ __forceinline__ void fd_finish(const FdecParams& p, uint8_t* smem, in
       }
     }
   }
-  if (single || p.defer_merge || p.keep_partials) return;
+  if (single || p.defer_merge) return;
 
   // ---- split-K combine by the last CTA of the row
   __threadfence();
@@ -339,9 +334,7 @@ __device__ __forceinline__ void fd_finish(const FdecParams& p, uint8_t* smem, in
   if (tid == 0) p.tickets[row_id] = 0;
 }
 
-// LOGITS: every scaled logit is also stored where p.logits is set (DENSE linear ranges; the
-// accumulated-weight decode, and the own tokens of the shared-prefix decode).
-template <int D, int NT, bool LOGITS = false>
+template <int D, int NT>
 __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const FdecParams p) {
   constexpr int ST = kFdStages;
   grid_dep_wait();  // the selection comes from the kernel before this one
@@ -487,8 +480,7 @@ __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const Fdec
     return (uint32_t)(half * (rows * 128) + r * 128 + ((cc ^ (r & 7)) << 4));
   };
   // one 16-token sub-tile: rows r0 .. r0 + 15 of the K / V tiles at kt / vt, nv >= 1 of them valid
-  // (jt: list entry of row r0)
-  auto sub_tile = [&](uint32_t kt, uint32_t vt, int rows, int r0, int nv, int jt) {
+  auto sub_tile = [&](uint32_t kt, uint32_t vt, int rows, int r0, int nv) {
     float s4[4] = {0.f, 0.f, 0.f, 0.f};
     {
       const int r = r0 + (lane & 7) + ((lane >> 3) & 1) * 8;
@@ -505,14 +497,6 @@ __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const Fdec
     const float x1 = ta < nv ? s4[1] * p.scale_log2 : -INFINITY;
     const float x2 = tb < nv ? s4[2] * p.scale_log2 : -INFINITY;
     const float x3 = tb < nv ? s4[3] * p.scale_log2 : -INFINITY;
-    if (LOGITS) {  // a DENSE linear range: list entry j is position j
-      const int qc = nt * 8 + 2 * (lane & 3);
-      if (p.logits && qc < p.logit_pitch) {
-        float* lg = p.logits + ((int64_t)g * p.T + off + jt) * p.logit_pitch + qc;
-        if (ta < nv) *reinterpret_cast<float2*>(lg + (int64_t)ta * p.logit_pitch) = make_float2(x0, x1);
-        if (tb < nv) *reinterpret_cast<float2*>(lg + (int64_t)tb * p.logit_pitch) = make_float2(x2, x3);
-      }
-    }
     float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
@@ -612,7 +596,7 @@ __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const Fdec
       __syncwarp();             // and so have the other lanes' (the tile mixes them)
       const int u = tg + WT * k;
       const uint32_t kt = wbase + (k % ST) * 2 * kSubBytes;
-      sub_tile(kt, kt + kSubBytes, 16, 0, ntok - u * 16, j0 + u * 16);
+      sub_tile(kt, kt + kSubBytes, 16, 0, ntok - u * 16);
       __syncwarp();             // every lane is done with the slot before it is refilled
     }
   } else {
@@ -630,7 +614,7 @@ __global__ void __launch_bounds__(fd_threads(NT)) flash_gather_kernel(const Fdec
         const int u = tg + WT * i;
         const int nv = ntok - (st * kFdTS + u * 16);  // valid tokens in this sub-tile
         if (nv <= 0) break;                           // warp-uniform
-        sub_tile(kt, vt, kFdTS, u * 16, nv, j0 + st * kFdTS + u * 16);
+        sub_tile(kt, vt, kFdTS, u * 16, nv);
       }
     }
   }

@@ -29,9 +29,7 @@
 // for fp32 outputs.
 #pragma once
 
-#include <cuda.h>
-
-#include "tcgen05.cuh"
+#include "dense_pass.cuh"
 
 namespace aoh {
 
@@ -65,6 +63,7 @@ struct alignas(64) TileParams {
   int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed;
   int32_t causal;            // 0: every row sees the whole group
   int32_t keep_partials;     // 1: partials also when splits == 1
+  int32_t late_wait;         // 1: the launch before is of the same call and writes nothing that is read here
   float scale_log2;          // > 0; a negative scale negates Q in the product
   uint32_t neg;
   uint8_t heads[kMaxHeads];
@@ -147,14 +146,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const uint32_t bar_q = bars + 8 * (2 * ST + 8), bar_fix = bars + 8 * (2 * ST + 9);
   const uint32_t bar_end = bars + 8 * (2 * ST + 10);
 
-  grid_dep_wait();
+  grid_dep_launch();
+  if (!p.late_wait) grid_dep_wait();
   if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y) == 0 && p.q_offsets[p.B] > p.total_q)
     record_error(kCheckPosition, p.B, p.q_offsets[p.B], p.total_q);  // rows past those of q are skipped
   int b, i0, n, q0;
   // later rows first, all heads of a tile together: the longest rows start first
   const int slot_id = (int)((gridDim.x - 1 - blockIdx.x) / p.n_listed), y = (int)(blockIdx.x % p.n_listed);
-  if (!ta_locate(p, slot_id, &b, &i0, &n, &q0)) return;
-  if (q0 + i0 >= p.total_q) return;  // (recorded above)
+  if (!ta_locate(p, slot_id, &b, &i0, &n, &q0) || q0 + i0 >= p.total_q) {  // (the latter is recorded above)
+    grid_dep_wait();
+    return;
+  }
   const int g = p.heads[y];
   const bool dense = p.roles[g] == 1;
   int off;
@@ -495,6 +497,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   }
   __syncthreads();
   if (warp == 10) tmem_dealloc<512>(tmem);
+  grid_dep_wait();  // with late_wait: what follows this kernel relies on the one before it, too
 }
 
 // ---------------------------------------------------------------------- joining partial rows
@@ -504,12 +507,9 @@ struct MergeParams {
   const int32_t* q_offsets;  // rows of every group ([B + 1]) or null: one group of all rows
   void* out;                 // bf16 or fp32 [total_q][Hq][D]
   int32_t B, Hq, G, total_q, splits, n_listed;
-  // partials of the split-K gather over the rows' own tokens, or null (row b is sequence b)
-  const float* own_ml;       // [b * n_listed + y][max_splits][NQP][2]
-  const float* own_acc;
-  const int32_t* offsets;
-  const int32_t* lengths;
-  int32_t chunk, max_splits, nqp;
+  // the rows' own tokens (row b is sequence b), or no own.pre; what one CTA finished is in out, not
+  // divided by its sum
+  DenseRows own;
   uint8_t heads[kMaxHeads];
 };
 
@@ -529,21 +529,26 @@ __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParam
   bool tiles = true;
   if (p.q_offsets) {  // rows that no group holds have no tile partials
     tiles = row >= p.q_offsets[0] && row < p.q_offsets[p.B];
-    if (!tiles && !p.own_ml) return;
+    if (!tiles && !p.own.pre) return;
     if (!tiles && hl == 0 && lane == 0) record_error(kCheckPosition, (int)row, -1, p.B);
   }
   const int ns = tiles ? p.splits : 0;
-  int no = 0;
-  if (p.own_ml) {
-    int off;
-    no = (seq_length(p.offsets, p.lengths, (int)row, false, &off) + p.chunk - 1) / p.chunk;
-  }
+  int no = 0, c0 = 0, c1 = 0;
+  if (p.own.pre && dense_row(p.own, p.n_listed, p.total_q, y, (int)row, &c0, &c1)) no = c1 - c0 + 1;
   const int64_t rows = (int64_t)p.total_q * p.Hq, tr = row * p.Hq + h;
-  const int64_t orow = ((row * p.n_listed + y) * p.max_splits) * p.nqp + hl % p.G;
-  auto at = [&](int s) { return s < ns ? s * rows + tr : orow + (int64_t)(s - ns) * p.nqp; };
+  auto ml_of = [&](int s) {
+    if (s < ns) return p.part_ml + (s * rows + tr) * 2;
+    const int64_t r = c0 == c1 ? (int64_t)y * p.total_q + row : dense_part(c0, s - ns);
+    return (c0 == c1 ? p.own.row_ml : p.own.part_ml) + (r * p.own.nqp + hl % p.G) * 2;
+  };
+  auto acc_of = [&](int s) {
+    if (s < ns) return p.part_acc + (s * rows + tr) * D;
+    if (c0 == c1) return static_cast<const float*>(p.out) + tr * D;
+    return p.own.part_acc + ((int64_t)dense_part(c0, s - ns) * p.own.nqp + hl % p.G) * D;
+  };
   const int nt = ns + no;
   float M = -INFINITY;
-  for (int s = lane; s < nt; s += 32) M = fmaxf(M, (s < ns ? p.part_ml : p.own_ml)[at(s) * 2]);
+  for (int s = lane; s < nt; s += 32) M = fmaxf(M, ml_of(s)[0]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[E], l = 0.f;
@@ -551,9 +556,8 @@ __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParam
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
 #pragma unroll 4
   for (int s = 0; s < nt; ++s) {
-    const int64_t i = at(s);
-    const float* ml = (s < ns ? p.part_ml : p.own_ml) + i * 2;
-    const float* a = (s < ns ? p.part_acc : p.own_acc) + i * D + lane * E;
+    const float* ml = ml_of(s);
+    const float* a = acc_of(s) + lane * E;
     const float w = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - M);
     l += w * ml[1];
 #pragma unroll
