@@ -480,8 +480,11 @@ def test_steps_launch_the_kernels():
     got = launches_of(lambda: ev(torch.rand((2, c.T), device="cuda"), None, d.lengths))
     assert got.pop("evict_key_kernel") == 1 and got.pop("evict_copy_kernel") == 1
     pfx = PrefixDecodeStep(c.k, c.v, c.offsets[:2], 700, 700, d.k, d.v, d.offsets, 128, d.T, 8, 0.1)
-    got = launches_of(lambda: pfx(q))
-    assert got.pop("tile_attend_kernel") == 1
+    assert launches_of(lambda: pfx(q)) == {"dense_pass_kernel": 1, "tile_merge_kernel": 1}  # few rows: one pass
+    many = Cache(185, [30] * 9, 2, 128)
+    pfx = PrefixDecodeStep(c.k, c.v, c.offsets[:2], 700, 700, many.k, many.v, many.offsets, 30, many.T, 8, 0.1)
+    assert launches_of(lambda: pfx(queries(186, 9, 8, 128).cuda())) == {
+        "tile_attend_kernel": 1, "dense_pass_kernel": 1, "tile_merge_kernel": 1}
     check_device()
     with pytest.raises(ValueError):
         pre(queries(184, 3, 8, 128).cuda(), i32([0, 1, 3]))

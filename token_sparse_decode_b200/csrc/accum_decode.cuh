@@ -16,7 +16,7 @@ namespace aoh {
 
 constexpr int kAmThreads = 256;
 constexpr int kAmTokens = 1024;               // tokens per CTA of the merge
-constexpr int kAmOut = 16;                    // float4 outputs per CTA
+constexpr int kAmOut = 64;                    // float4 outputs per CTA
 constexpr int kAmGroups = kAmThreads / kAmOut;
 
 struct AccumParams {
@@ -95,15 +95,33 @@ __global__ void __launch_bounds__(kAmThreads) accum_merge_kernel(const AccumPara
     const float* mi = p.mass_in ? p.mass_in + (int64_t)g * p.T + off : nullptr;
     float* mo = p.mass_out + (int64_t)g * p.T + off;
     const float* lg = p.logits + ((int64_t)g * p.T + off) * p.logit_pitch;
-    for (int t = t0 + tid; t < t1; t += kAmThreads) {
-      const float2* row = reinterpret_cast<const float2*>(lg + (int64_t)t * p.logit_pitch);
-      float s = 0.f;
-      for (int q = 0; q < p.G; q += 2) {
-        const float2 x = __ldcg(row + (q >> 1));
-        s += exp2f(x.x - sM[q]) * sInv[q];
-        if (q + 1 < p.G) s += exp2f(x.y - sM[q + 1]) * sInv[q + 1];
+    constexpr int PT = kAmTokens / kAmThreads;  // tokens of a thread, their loads in flight together
+    float w[PT], old[PT];
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int t = t0 + tid + i * kAmThreads;
+      w[i] = 0.f;
+      old[i] = mi && t < t1 ? mi[t] : 0.f;
+    }
+    for (int q = 0; q < p.G; q += 2) {
+      float2 x[PT];
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        const int t = t0 + tid + i * kAmThreads;
+        x[i] = t < t1 ? __ldcg(reinterpret_cast<const float2*>(lg + (int64_t)t * p.logit_pitch + q)) : make_float2(-INFINITY, -INFINITY);
       }
-      mo[t] = mi ? fmaf(p.decay, mi[t], s) : s;
+      const bool two = q + 1 < p.G;
+      const float M0 = sM[q], I0 = sInv[q], M1 = two ? sM[q + 1] : 0.f, I1 = two ? sInv[q + 1] : 0.f;
+#pragma unroll
+      for (int i = 0; i < PT; ++i) {
+        w[i] += ex2(x[i].x - M0) * I0;
+        if (two) w[i] += ex2(x[i].y - M1) * I1;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int t = t0 + tid + i * kAmThreads;
+      if (t < t1) mo[t] = mi ? fmaf(p.decay, old[i], w[i]) : w[i];
     }
   }
 

@@ -1868,20 +1868,25 @@ aoh_status encode_cache(CUtensorMap* k, CUtensorMap* v, const aoh_kv_cache* kv, 
 // ---- one pass over a whole cache (accumulated weights; the own tokens behind a shared prefix)
 struct DenseWs {
   int nqp, ctas;
-  size_t off_row, off_ml, off_acc, total;
+  size_t off_row, off_ml, off_acc, off_row_acc, total;
 };
 
-DenseWs dense_ws(const aoh_kv_cache* kv, int32_t Hq) {
+// `pieces` per SM: one where the pass runs alone, two where it fills SMs beside another kernel.
+// With `prefix` its rows (nq query rows each) come first in the same pass.
+DenseWs dense_ws(const aoh_kv_cache* kv, int32_t nq, int pieces, const aoh_kv_cache* prefix = nullptr) {
   DenseWs w{};
-  const int G = Hq / kv->n_kv_heads;
-  w.nqp = G <= 8 ? 8 : (G <= 16 ? 16 : 32);
+  w.nqp = nq <= 8 ? 8 : (nq <= 16 ? 16 : 32);
   uint8_t heads[kMaxHeads];
-  const int64_t rows = int64_t(kv->batch) * stored_heads(kv, heads);
-  w.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), rows * ceil_div(kv->max_len, kDpTile)));
-  w.off_row = align256(sizeof(int32_t) * ((size_t)kv->batch + 1));
-  w.off_ml = w.off_row + align256(sizeof(float) * 2 * (size_t)rows * w.nqp);
+  const int64_t listed = stored_heads(kv, heads), seqs = int64_t(kv->batch) + (prefix ? prefix->batch : 0);
+  int64_t tiles = kv->batch * ceil_div(kv->max_len, kDpTile);
+  if (prefix) tiles += prefix->batch * ceil_div(prefix->max_len, kDpTile);
+  w.ctas = (int)std::max<int64_t>(1, std::min<int64_t>(int64_t(pieces) * sm_count(), listed * tiles));
+  w.off_row = align256(sizeof(int32_t) * ((size_t)seqs + 1));
+  w.off_ml = w.off_row + align256(sizeof(float) * 2 * (size_t)(listed * seqs) * w.nqp);
   w.off_acc = w.off_ml + align256(sizeof(float) * 4 * (size_t)w.ctas * w.nqp);
-  w.total = w.off_acc + align256(sizeof(float) * 2 * (size_t)w.ctas * w.nqp * kv->head_dim);
+  w.off_row_acc = w.off_acc + align256(sizeof(float) * 2 * (size_t)w.ctas * w.nqp * kv->head_dim);
+  w.total = w.off_row_acc;
+  if (prefix) w.total += align256(sizeof(float) * (size_t)(listed * seqs) * w.nqp * kv->head_dim);
   return w;
 }
 
@@ -1900,10 +1905,19 @@ aoh_status launch_dense_t(const DenseParams& dp, int ctas, cudaStream_t st) {
 
 // Launches the pass over every stored head; `rows` says where its results are.
 aoh_status launch_dense(const void* q, int32_t Hq, const aoh_kv_cache* kv, float scale, float* out, bool normalise,
-                        float* logits, int logit_pitch, const DenseWs& w, uint8_t* ws, DenseRows* rows, cudaStream_t st) {
+                        float* logits, int logit_pitch, bool late_wait, const DenseWs& w, uint8_t* ws, DenseRows* rows,
+                        cudaStream_t st, const aoh_kv_cache* prefix = nullptr, const int32_t* seq_start = nullptr) {
   DenseParams dp{};
-  aoh_status s = encode_cache(&dp.kmap, &dp.vmap, kv, kDpTile);
-  if (s != AOH_OK) return s;
+  aoh_status s = encode_cache(&dp.kmap[0], &dp.vmap[0], kv, kDpTile);
+  if (s != AOH_OK || (prefix && (s = encode_cache(&dp.kmap[1], &dp.vmap[1], prefix, kDpTile)) != AOH_OK)) return s;
+  if (prefix) {
+    dp.pre_offsets = prefix->offsets;
+    dp.pre_lengths = prefix->lengths;
+    dp.seq_start = seq_start;
+    dp.NP = prefix->batch;
+    for (int g = 0; g < kv->n_kv_heads; ++g) dp.pre_slot[g] = slot_of(prefix, g);
+    dp.row_acc = reinterpret_cast<float*>(ws + w.off_row_acc);
+  }
   dp.q = static_cast<const uint16_t*>(q);
   dp.offsets = kv->offsets;
   bind_cache(dp, kv);
@@ -1920,15 +1934,20 @@ aoh_status launch_dense(const void* q, int32_t Hq, const aoh_kv_cache* kv, float
   dp.Hq = Hq;
   dp.G = Hq / kv->n_kv_heads;
   dp.normalise = normalise;
+  dp.late_wait = late_wait;
   dp.scale_log2 = scale * 1.4426950408889634f;
-  dp.planned = kv->batch > kDpSeqs;
+  dp.planned = kv->batch + dp.NP > kDpSeqs;
   rows->pre = dp.pre;
   rows->row_ml = dp.row_ml;
   rows->part_ml = dp.part_ml;
   rows->part_acc = dp.part_acc;
+  rows->row_acc = dp.row_acc ? dp.row_acc : out;
+  rows->packed = dp.row_acc != nullptr;
+  rows->NP = dp.NP;
   rows->C = w.ctas;
   rows->nqp = w.nqp;
   if (dp.planned) {
+    dp.late_wait = 0;  // the plan is waited for
     const PlanParams pp{kv->offsets, kv->lengths, dp.pre, kv->batch};
     if ((s = launch_dependent(dense_plan_kernel, dim3(1), 1024, 0, 0, st, pp)) != AOH_OK ||
         (s = count_launch(AOH_KERNEL_DENSE_PLAN, st)) != AOH_OK)
@@ -1956,12 +1975,14 @@ int list_by_role(const aoh_kv_cache* kv, const uint8_t* roles, uint8_t* out) {
 }
 
 struct TileWs {
-  int slots, splits;
+  int slots, splits, segments;
   size_t off_acc, total;
 };
 
 // The grid of a tile call: a slot per two tiles of rows of every group, times the heads, times as
-// many splits of the key range as give every SM a CTA (at least four key tiles each).
+// many splits of the key range as give every SM a CTA, of at least four key tiles each, or, where every
+// split leaves partials anyway, of a partial's (64 sequences behind 8192 tokens, with the pass over their
+// own tokens on the other SMs: 18 splits 77 us, 10 68 us, 8 66 us).
 TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, const uint8_t* roles, int32_t sink,
                int32_t window, int bn, bool keep) {
   TileWs w{};
@@ -1977,9 +1998,12 @@ TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, 
     longest = std::max(longest, r == AOH_ROLE_DENSE ? L : std::min<int64_t>(L, int64_t(sink) + window + P2));
   }
   const int64_t ctas = std::max<int64_t>(1, int64_t(w.slots) * n_listed);
-  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count() / ctas, ceil_div(longest, bn) / 4));
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count() / ctas, ceil_div(longest, bn) / (keep ? kTaSegment : 4)));
+  // (a bound for the tiles of a split: a key range's share, rounded up)
+  w.segments = keep ? (int)ceil_div(ceil_div(ceil_div(longest, bn), w.splits), kTaSegment) : 1;
+  w.segments = std::max(w.segments, 1);
   if (w.splits > 1 || keep) {
-    const size_t rows = (size_t)w.splits * (size_t)total_q * Hq;
+    const size_t rows = (size_t)w.splits * w.segments * (size_t)total_q * Hq;
     w.off_acc = align256(sizeof(float) * 2 * rows);
     w.total = w.off_acc + align256(sizeof(float) * rows * kv->head_dim);
   }
@@ -2002,6 +2026,7 @@ aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_ca
   tp.PT = PT;
   tp.total_q = (int)total_q;
   tp.splits = w.splits;
+  tp.segments = w.segments;
   // a positive factor: masked scores are -inf before they are scaled, and -inf * 0 is a NaN
   tp.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);
   tp.neg = scale < 0.f;
@@ -2035,20 +2060,21 @@ void bind_merge(MergeParams& mp, const TileParams& tp, int n_listed, void* out) 
   mp.Hq = tp.Hq;
   mp.G = tp.G;
   mp.total_q = tp.total_q;
-  mp.splits = tp.splits;
+  mp.splits = tp.splits * tp.segments;
   mp.n_listed = n_listed;
   memcpy(mp.heads, tp.heads, sizeof(mp.heads));
 }
 
 template <int D, bool BF16>
 aoh_status launch_merge(const MergeParams& mp, cudaStream_t st) {
-  const int64_t blocks = ceil_div(int64_t(mp.total_q) * mp.n_listed * mp.G, kTmThreads / 32);
+  const int64_t blocks = int64_t(mp.total_q) * mp.n_listed * mp.G;
   aoh_status s = launch_dependent(tile_merge_kernel<D, BF16>, dim3((unsigned)blocks), kTmThreads, 0, 0, st, mp);
   return s != AOH_OK ? s : count_launch(AOH_KERNEL_TILE_MERGE, st);
 }
 
 // Shared prefixes: [pass over the sequences' own tokens][tile partials]
 struct PrefixWs {
+  bool few;  // all rows of a prefix fit the few query rows of the dense pass
   DenseWs own;
   TileWs tiles;
   size_t off_tiles, total;
@@ -2056,7 +2082,17 @@ struct PrefixWs {
 
 PrefixWs prefix_ws(const aoh_kv_cache* prefix, const aoh_kv_cache* kv, int32_t Hq) {
   PrefixWs w{};
-  w.own = dense_ws(kv, Hq);
+  const int G = Hq / kv->n_kv_heads;
+  // Up to 32 rows behind a prefix: its tokens go through the dense pass, in one launch with the
+  // sequences' own (4 rows behind 512 tokens: 15 us by tiles, 10 us so; the tiles' products always have
+  // 128 rows, and their CTAs take 8 us to begin and end).
+  w.few = int64_t(kv->batch) * G <= kMaxQRows && prefix->batch + kv->batch <= kDpSeqs;
+  if (w.few) {
+    w.own = dense_ws(kv, kv->batch * G, 1, prefix);
+    w.total = w.own.total;
+    return w;
+  }
+  w.own = dense_ws(kv, G, 2);
   w.tiles = tile_ws(prefix, Hq, kv->batch, prefix->batch, nullptr, 0, 0, TaTile<128, 3>::BN, true);
   w.off_tiles = w.own.total;
   w.total = w.off_tiles + w.tiles.total;
@@ -2072,7 +2108,7 @@ struct AccumWs {
 
 AccumWs accum_ws(const aoh_kv_cache* kv, int32_t Hq) {
   AccumWs w{};
-  w.pass = dense_ws(kv, Hq);
+  w.pass = dense_ws(kv, Hq / kv->n_kv_heads, 1);
   w.pitch = (Hq / kv->n_kv_heads + 1) & ~1;
   w.total = w.pass.total + align256(sizeof(float) * (size_t)kv->n_kv_heads * (size_t)kv->total_tokens * w.pitch);
   return w;
@@ -2164,19 +2200,32 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
   const int n_listed = stored_heads(kv, heads);
   if (n_listed == 0) return AOH_OK;
   MergeParams mp{};
-  // the sequences' own tokens; what one CTA finishes of them waits in out for the merge
-  if ((s = launch_dense(q, n_q_heads, kv, scale, out, false, nullptr, 0, w.own, ws, &mp.own, st)) != AOH_OK) return s;
+  if (w.few) {
+    if ((s = launch_dense(q, n_q_heads, kv, scale, out, false, nullptr, 0, false, w.own, ws, &mp.own, st, prefix, seq_start)) !=
+        AOH_OK)
+      return s;
+    mp.q_offsets = seq_start;
+    mp.out = out;
+    mp.B = prefix->batch;
+    mp.Hq = n_q_heads;
+    mp.G = n_q_heads / kv->n_kv_heads;
+    mp.total_q = kv->batch;
+    mp.n_listed = n_listed;
+    memcpy(mp.heads, heads, sizeof(mp.heads));
+    return kv->head_dim == 128 ? launch_merge<128, false>(mp, st) : launch_merge<64, false>(mp, st);
+  }
   // the prefixes: tiles of the sequences' rows
   TileParams tp{};
   stored_heads(prefix, tp.heads);
   if ((s = bind_tiles(tp, q, n_q_heads, prefix, seq_start, kv->batch, scale, w.tiles, ws + w.off_tiles,
                       TaTile<128, 3>::BN)) != AOH_OK)
     return s;
-  tp.keep_partials = 1;
-  tp.late_wait = 1;
   memset(tp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
   s = kv->head_dim == 128 ? launch_tiles<128, 3>(tp, w.tiles, n_listed, st) : launch_tiles<64, 3>(tp, w.tiles, n_listed, st);
   if (s != AOH_OK || (s = count_launch(AOH_KERNEL_TILE_ATTEND, st)) != AOH_OK) return s;
+  // the sequences' own tokens, beside the tiles on SMs that these leave; what one CTA finishes of them
+  // waits in out for the merge
+  if ((s = launch_dense(q, n_q_heads, kv, scale, out, false, nullptr, 0, true, w.own, ws, &mp.own, st)) != AOH_OK) return s;
   bind_merge(mp, tp, n_listed, out);
   return kv->head_dim == 128 ? launch_merge<128, false>(mp, st) : launch_merge<64, false>(mp, st);
 }
@@ -2203,7 +2252,7 @@ aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* logits = reinterpret_cast<float*>(ws + w.pass.total);
   cudaStream_t st = as_stream(stream);
-  if ((s = launch_dense(q, n_q_heads, kv, scale, out, true, logits, w.pitch, w.pass, ws, &ap.rows, st)) != AOH_OK) return s;
+  if ((s = launch_dense(q, n_q_heads, kv, scale, out, true, logits, w.pitch, false, w.pass, ws, &ap.rows, st)) != AOH_OK) return s;
   ap.offsets = kv->offsets;
   ap.lengths = kv->lengths;
   ap.logits = logits;

@@ -16,7 +16,9 @@
 // One warp copies K and V tiles by TMA (128-byte swizzle) into a ring; eight warps take 16-token
 // sub-tiles, tokens on the M side of mma.m16n8k16 (the query rows are the N side: 7 rows fill 7 of
 // 8 columns).  Weights enter the product with V as three bf16 terms, so that fp32 outputs keep
-// fp32 weights.  Bound by the K / V bytes.
+// fp32 weights, and every sub-tile's product starts from zero and is added by the FMA units: the
+// tensor cores' own accumulation rounds towards zero, 3e-6 along 900 tokens.  Bound by the K / V
+// bytes.
 #pragma once
 
 #include <cuda.h>
@@ -41,40 +43,68 @@ struct DpTile {
 };
 
 struct alignas(64) DenseParams {
-  CUtensorMap kmap, vmap;
+  CUtensorMap kmap[2], vmap[2];  // the sequences' cache, the prefixes'
   const uint16_t* q;         // [B][Hq][D]
   const int32_t* offsets;
   const int32_t* lengths;    // or null
-  int32_t* pre;              // [B + 1] tiles before sequence b of one head
-  float* out;                // fp32 [B][Hq][D]: rows of one CTA
-  float* row_ml;             // [n_listed][B][NQP][2]: (m, l) of the same
+  int32_t* pre;              // [NP + B + 1] tiles of one head before entry v
+  float* out;                // fp32 [B][Hq][D]: rows of one CTA, unless row_acc
+  float* row_acc;            // [n_listed][NP + B][NQP][D] or null
+  float* row_ml;             // [n_listed][NP + B][NQP][2]: (m, l) of the same
   float* part_ml;            // [2 C][NQP][2]
   float* part_acc;           // [2 C][NQP][D]
   float* logits;             // [Hkv][T][logit_pitch] or null
   int64_t T;
   int32_t logit_pitch;       // even, >= NQ
   int32_t B, Hq, G, n_listed;
-  int32_t planned;           // 1: pre is there already
+  // Entries 0 .. NP - 1 of the line are shared prefixes, whose query rows are those of the sequences
+  // [seq_start[v], seq_start[v + 1]) (null: all), G each; the sequences follow.
+  int32_t NP;
+  const int32_t* pre_offsets;
+  const int32_t* pre_lengths;
+  const int32_t* seq_start;
+  int32_t planned;           // 1: pre is there already (only with NP = 0)
   int32_t normalise;         // 1: out = acc / l, 0: acc
+  int32_t late_wait;         // 1: the launch before is of the same call (it waited for what came before the
+                             //    call) and writes nothing that is read here: run beside it, and end after it
   float scale_log2;
   uint8_t heads[kMaxHeads];
   uint8_t slot[kMaxHeads];
+  uint8_t pre_slot[kMaxHeads];
 };
 
-// Tiles before every sequence of one head, by one block
-__device__ __forceinline__ void dense_plan(const int32_t* offsets, const int32_t* lengths, int B, int32_t* pre, int tid,
-                                           int threads, int* scratch, bool sync_all) {
+// Entry v of the line: its length, first token, first sequence and query rows
+struct DenseEntry {
+  int L, off, seq, nq;
+};
+__device__ __forceinline__ DenseEntry dense_entry(const DenseParams& p, int v) {
+  DenseEntry e;
+  if (v >= p.NP) {
+    e.seq = v - p.NP;
+    e.nq = p.G;
+    e.L = seq_length(p.offsets, p.lengths, e.seq, false, &e.off);
+  } else {
+    e.seq = p.seq_start ? max(0, min(p.seq_start[v], p.B)) : 0;
+    const int end = p.seq_start ? max(e.seq, min(p.seq_start[v + 1], p.B)) : p.B;
+    e.nq = (end - e.seq) * p.G;
+    e.L = seq_length(p.pre_offsets, p.pre_lengths, v, false, &e.off);
+    if (e.nq == 0) e.L = 0;  // nobody continues it
+  }
+  return e;
+}
+
+// Tiles before every entry: an exclusive sum by one block
+template <typename Len>
+__device__ __forceinline__ void dense_plan(Len len, int n, int32_t* pre, int tid, int threads, int* scratch) {
   int base = 0;
-  for (int b0 = 0; b0 < B; b0 += threads) {
-    int n = 0, off;
-    if (b0 + tid < B) n = (seq_length(offsets, lengths, b0 + tid, false, &off) + kDpTile - 1) / kDpTile;
+  for (int v0 = 0; v0 < n; v0 += threads) {
+    const int c = v0 + tid < n ? (len(v0 + tid) + kDpTile - 1) / kDpTile : 0;
     int total;
-    const int at = block_exclusive_scan(n, scratch, &total);
-    if (b0 + tid < B) pre[b0 + tid] = base + at;
+    const int at = block_exclusive_scan(c, scratch, &total);
+    if (v0 + tid < n) pre[v0 + tid] = base + at;
     base += total;
   }
-  if (tid == 0) pre[B] = base;
-  if (sync_all) __syncthreads();
+  if (tid == 0) pre[n] = base;
 }
 
 struct PlanParams {
@@ -86,7 +116,10 @@ struct PlanParams {
 __global__ void __launch_bounds__(1024) dense_plan_kernel(const PlanParams p) {
   grid_dep_wait();
   __shared__ int scratch[33];
-  dense_plan(p.offsets, p.lengths, p.B, p.pre, threadIdx.x, 1024, scratch, false);
+  dense_plan([&](int v) {
+    int off;
+    return seq_length(p.offsets, p.lengths, v, false, &off);
+  }, p.B, p.pre, threadIdx.x, 1024, scratch);
 }
 
 // The piece of CTA c: [dense_piece(n, c, C), dense_piece(n, c + 1, C)) of n tiles
@@ -129,20 +162,25 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
     mbar_init_fence();
     s_stop = 0;
   }
-  grid_dep_wait();
+  if (!p.late_wait) grid_dep_wait();
   grid_dep_launch();
+  const int nv = p.NP + p.B;
   const int32_t* pre = p.pre;
   if (!p.planned) {
-    dense_plan(p.offsets, p.lengths, p.B, s_pre, tid, kDpThreads, s_scan, true);
+    dense_plan([&](int v) { return dense_entry(p, v).L; }, nv, s_pre, tid, kDpThreads, s_scan);
+    __syncthreads();
     pre = s_pre;
     if (blockIdx.x == 0)
-      for (int b = tid; b <= p.B; b += kDpThreads) p.pre[b] = s_pre[b];
+      for (int v = tid; v <= nv; v += kDpThreads) p.pre[v] = s_pre[v];
   }
   __syncthreads();
-  const int per_head = pre[p.B], c = blockIdx.x;
+  const int per_head = pre[nv], c = blockIdx.x;
   const int64_t n_all = (int64_t)per_head * p.n_listed;
   const int C = (int)min((int64_t)gridDim.x, n_all);  // no piece is empty
-  if (c >= C) return;
+  if (c >= C) {
+    if (p.late_wait && c == 0) grid_dep_wait();
+    return;
+  }
   const int64_t w0 = dense_piece(n_all, c, C), w1 = dense_piece(n_all, c + 1, C);
   volatile int* stop = &s_stop;
 
@@ -150,9 +188,12 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
     int i = 0;
     bool ok = true;
     for (int64_t w = w0; w < w1 && ok;) {
-      const int y = (int)(w / per_head), x = (int)(w % per_head), b = dense_seq(pre, p.B, x);
-      const int n = (int)min((int64_t)(pre[b + 1] - x), w1 - w);
-      const int tok = p.offsets[b] + (x - pre[b]) * kDpTile, slot = p.slot[p.heads[y]];
+      const int y = (int)(w / per_head), x = (int)(w % per_head), v = dense_seq(pre, nv, x);
+      const int n = (int)min((int64_t)(pre[v + 1] - x), w1 - w);
+      const bool own = v >= p.NP;
+      const int tok = (own ? p.offsets[v - p.NP] : p.pre_offsets[v]) + (x - pre[v]) * kDpTile;
+      const int slot = own ? p.slot[p.heads[y]] : p.pre_slot[p.heads[y]];
+      const CUtensorMap *km = &p.kmap[own ? 0 : 1], *vm = &p.vmap[own ? 0 : 1];
       for (int t = 0; t < n; ++t, ++i) {
         const int s = i % ST;
         if (!(ok = warp_wait(bar_empty(s), ((i / ST) & 1) ^ 1, stop))) break;
@@ -161,8 +202,8 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
           mbar_expect_tx(bar_full(s), T::kStage);
 #pragma unroll
           for (int h = 0; h < D / 64; ++h) {
-            tma_load_3d(dst + h * T::kHalf, &p.kmap, h * 64, slot, tok + t * kDpTile, bar_full(s));
-            tma_load_3d(dst + T::kTile + h * T::kHalf, &p.vmap, h * 64, slot, tok + t * kDpTile, bar_full(s));
+            tma_load_3d(dst + h * T::kHalf, km, h * 64, slot, tok + t * kDpTile, bar_full(s));
+            tma_load_3d(dst + T::kTile + h * T::kHalf, vm, h * 64, slot, tok + t * kDpTile, bar_full(s));
           }
         }
         __syncwarp();
@@ -177,18 +218,18 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
     int i = 0;
     bool ok = true;
     for (int64_t w = w0; w < w1;) {
-      const int y = (int)(w / per_head), x = (int)(w % per_head), b = dense_seq(pre, p.B, x), g = p.heads[y];
-      const int t0 = x - pre[b], n = (int)min((int64_t)(pre[b + 1] - x), w1 - w);
-      int off;
-      const int L = seq_length(p.offsets, p.lengths, b, false, &off);
+      const int y = (int)(w / per_head), x = (int)(w % per_head), v = dense_seq(pre, nv, x), g = p.heads[y];
+      const int t0 = x - pre[v], n = (int)min((int64_t)(pre[v + 1] - x), w1 - w);
+      const DenseEntry en = dense_entry(p, v);
+      const int L = en.L, off = en.off, nq = min(en.nq, NQP);
       uint32_t bq[KS][2];  // Q as B fragments: column lane / 4 of the n-tile
       {
         const int qr = nt * 8 + (lane >> 2);
-        const uint16_t* qp = p.q + ((int64_t)b * p.Hq + g * p.G + qr) * D + 2 * (lane & 3);
+        const uint16_t* qp = p.q + ((int64_t)(en.seq + qr / p.G) * p.Hq + g * p.G + qr % p.G) * D + 2 * (lane & 3);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          bq[ks][0] = qr < p.G ? *reinterpret_cast<const uint32_t*>(qp + ks * 16) : 0u;
-          bq[ks][1] = qr < p.G ? *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8) : 0u;
+          bq[ks][0] = qr < nq ? *reinterpret_cast<const uint32_t*>(qp + ks * 16) : 0u;
+          bq[ks][1] = qr < nq ? *reinterpret_cast<const uint32_t*>(qp + ks * 16 + 8) : 0u;
         }
       }
       float acc[KS][4];
@@ -277,8 +318,11 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
             for (int mt = 0; mt < KS; ++mt) {
               uint32_t a[4];
               ldsm_x4_trans(a, vt + tile_off(r, mt * 16 + dsel));
+              float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int part = 0; part < 3; ++part) mma_16816(acc[mt], a, pa[part], pb[part]);
+              for (int part = 2; part >= 0; --part) mma_16816(o, a, pa[part], pb[part]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[mt][e] += o[e];
             }
           }
         }
@@ -309,10 +353,10 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
         }
       }
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
-      const bool before = t0 > 0, after = x + n < pre[b + 1], cut = before || after;
+      const bool before = t0 > 0, after = x + n < pre[v + 1], cut = before || after;
       const int64_t part = 2 * c + (before ? 0 : 1);
-      float* ml = cut ? p.part_ml + part * NQP * 2 : p.row_ml + ((int64_t)y * p.B + b) * NQP * 2;
-      for (int e = tid; e < p.G * (D / 4); e += 32 * kDpWarps) {
+      float* ml = cut ? p.part_ml + part * NQP * 2 : p.row_ml + ((int64_t)y * nv + v) * NQP * 2;
+      for (int e = tid; e < nq * (D / 4); e += 32 * kDpWarps) {
         const int qr = e / (D / 4), dd = (e % (D / 4)) * 4, ntq = qr >> 3, cq = qr & 7;
         float M = -INFINITY, Ls = 0.f;
 #pragma unroll
@@ -322,20 +366,21 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
         for (int t = 0; t < WT; ++t) {
           const int ws = (ntq + NT * t) * 8 + cq;
           const float f = red_ml[ws * 2] == -INFINITY ? 0.f : ex2(red_ml[ws * 2] - M);
-          const float4 v = *reinterpret_cast<const float4*>(red_acc + ws * D + dd);
+          const float4 a4 = *reinterpret_cast<const float4*>(red_acc + ws * D + dd);
           Ls += f * red_ml[ws * 2 + 1];
-          A.x += f * v.x;
-          A.y += f * v.y;
-          A.z += f * v.z;
-          A.w += f * v.w;
+          A.x += f * a4.x;
+          A.y += f * a4.y;
+          A.z += f * a4.z;
+          A.w += f * a4.w;
         }
         if (dd == 0) *reinterpret_cast<float2*>(ml + qr * 2) = make_float2(M, Ls);
         if (cut) {
           *reinterpret_cast<float4*>(p.part_acc + (part * NQP + qr) * D + dd) = A;
         } else {
           const float inv = p.normalise ? 1.f / Ls : 1.f;
-          *reinterpret_cast<float4*>(p.out + ((int64_t)b * p.Hq + g * p.G + qr) * D + dd) =
-              make_float4(A.x * inv, A.y * inv, A.z * inv, A.w * inv);
+          float* o = p.row_acc ? p.row_acc + (((int64_t)y * nv + v) * NQP + qr) * D
+                               : p.out + ((int64_t)en.seq * p.Hq + g * p.G + qr) * D;
+          *reinterpret_cast<float4*>(o + dd) = make_float4(A.x * inv, A.y * inv, A.z * inv, A.w * inv);
         }
       }
       asm volatile("bar.sync 1, 256;\n" ::: "memory");
@@ -349,19 +394,23 @@ __global__ void __launch_bounds__(kDpThreads, 1) dense_pass_kernel(const __grid_
     for (int e = 0; e < (1 << 16); ++e) __nanosleep(20);
   }
   __syncthreads();
+  // what follows this kernel relies on the one before it, too; one block that waits for it will do
+  if (p.late_wait && blockIdx.x == 0) grid_dep_wait();
 }
 
 // ---------------------------------------------------------------------- where a row's results are
 struct DenseRows {
   const int32_t* pre;
   const float* row_ml;
+  const float* row_acc;      // packed: [n_listed][NP + B][NQP][D], else out: [B][Hq][D]
   const float* part_ml;
   const float* part_acc;
   int32_t C, nqp;            // CTAs launched
+  int32_t packed, NP;
 };
-// The CTAs [c0, c1] that hold pieces of row (y, b); false: the row is empty
-__device__ __forceinline__ bool dense_row(const DenseRows& d, int n_listed, int B, int y, int b, int* c0, int* c1) {
-  const int per_head = d.pre[B], a = d.pre[b], e = d.pre[b + 1];
+// The CTAs [c0, c1] that hold pieces of head y's entry v (of nv); false: it is empty
+__device__ __forceinline__ bool dense_row(const DenseRows& d, int n_listed, int nv, int y, int v, int* c0, int* c1) {
+  const int per_head = d.pre[nv], a = d.pre[v], e = d.pre[v + 1];
   if (a == e) return false;
   const int64_t n = (int64_t)per_head * n_listed, f = (int64_t)y * per_head;
   const int C = (int)min((int64_t)d.C, n);

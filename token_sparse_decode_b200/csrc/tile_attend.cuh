@@ -25,25 +25,31 @@
 // depend on m), which is as good as never after a row's first tile.
 //
 // Weights in the product with V: PARTS = 1 rounds them to bf16 (2^-9 relative, of the order of the
-// rounding of a bf16 output); PARTS = 3 keeps 24 bits as three bf16 terms, each multiplied with V,
-// for fp32 outputs.
+// rounding of a bf16 output); PARTS = 3, for fp32 outputs, keeps 24 bits as three bf16 terms, each
+// multiplied with V (two terms and key tiles of 128 were a tenth faster and twice as far off).  The
+// accumulation in TMEM drops the bits below the accumulator's last, always towards zero, which adds
+// up along a row (9e-6 after 3600 tokens): with PARTS = 3 a row's O is therefore taken out as a partial
+// of its own after every kTaSegment key tiles.
 #pragma once
+
+#include <type_traits>
 
 #include "dense_pass.cuh"
 
 namespace aoh {
 
 constexpr int kTaThreads = 384;       // softmax of tile 0, of tile 1, and a warpgroup of load / MMA warps
-constexpr int kTaRegsSoftmax = 216;   // 2 x 128 x 216 + 128 x 72 = 384 x 168 registers
-constexpr int kTaRegsOther = 72;
+constexpr int kTaRegsSoftmax = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 registers
+constexpr int kTaRegsOther = 88;
 constexpr int kTaRegsLaunch = 168;
 constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
+constexpr int kTaSegment = 16;        // key tiles of a partial (PARTS > 1)
 constexpr float kTaGrowth = 60.f;     // log2 of the largest weight before a rescale
 
 template <int D, int PARTS>
 struct TaTile {
   static constexpr int BN = PARTS == 1 ? 128 : 64;  // tokens per K / V tile: 128 columns hold S and the P parts
-  static constexpr int C0 = PARTS == 1 ? 64 : 32;   // tokens whose weights go to the product first, while the
+  static constexpr int C0 = BN / 2;                 // tokens whose weights go to the product first, while the
                                                     // others' are computed
   static constexpr int kQBytes = 128 * D * 2;
   static constexpr int kKvBytes = BN * D * 2;
@@ -58,12 +64,11 @@ struct alignas(64) TileParams {
   const int32_t* lengths;    // [B] or null
   const int32_t* q_offsets;  // [B + 1] rows of every group, or null: one group of all rows
   uint16_t* out;             // splits == 1: bf16 [total_q][Hq][D]
-  float* part_ml;            // else (m, l) [splits][total_q][Hq][2], m times scale_log2
-  float* part_acc;           //      [splits][total_q][Hq][D]
+  float* part_ml;            // else (m, l) [splits][segments][total_q][Hq][2], m times scale_log2
+  float* part_acc;           //      [splits][segments][total_q][Hq][D]
   int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed;
+  int32_t segments;          // partials of a split (PARTS > 1)
   int32_t causal;            // 0: every row sees the whole group
-  int32_t keep_partials;     // 1: partials also when splits == 1
-  int32_t late_wait;         // 1: the launch before is of the same call and writes nothing that is read here
   float scale_log2;          // > 0; a negative scale negates Q in the product
   uint32_t neg;
   uint8_t heads[kMaxHeads];
@@ -146,17 +151,15 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const uint32_t bar_q = bars + 8 * (2 * ST + 8), bar_fix = bars + 8 * (2 * ST + 9);
   const uint32_t bar_end = bars + 8 * (2 * ST + 10);
 
+  grid_dep_wait();
   grid_dep_launch();
-  if (!p.late_wait) grid_dep_wait();
   if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y) == 0 && p.q_offsets[p.B] > p.total_q)
     record_error(kCheckPosition, p.B, p.q_offsets[p.B], p.total_q);  // rows past those of q are skipped
   int b, i0, n, q0;
   // later rows first, all heads of a tile together: the longest rows start first
   const int slot_id = (int)((gridDim.x - 1 - blockIdx.x) / p.n_listed), y = (int)(blockIdx.x % p.n_listed);
-  if (!ta_locate(p, slot_id, &b, &i0, &n, &q0) || q0 + i0 >= p.total_q) {  // (the latter is recorded above)
-    grid_dep_wait();
-    return;
-  }
+  if (!ta_locate(p, slot_id, &b, &i0, &n, &q0)) return;
+  if (q0 + i0 >= p.total_q) return;  // (recorded above)
   const int g = p.heads[y];
   const bool dense = p.roles[g] == 1;
   int off;
@@ -178,6 +181,8 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const int n_all = a1 + max(0, b1 - b0);
   const int j_lo = (int)((int64_t)n_all * blockIdx.y / p.splits);
   const int n_it = (int)((int64_t)n_all * (blockIdx.y + 1) / p.splits) - j_lo;
+  // O is taken out after key tile j
+  auto last_of = [&](int j) { return j + 1 == n_it || (PARTS > 1 && (j + 1) % kTaSegment == 0); };
   auto key_tile = [&](int j) { return (j_lo + j < a1 ? j_lo + j : b0 + j_lo + j - a1) * BN; };
 
   if (tid == 0) {
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
         __syncwarp();
         int sv = 1, ph = 0;  // stage and phase of V_j; K_{j+1} is in the next one
         for (int j = 0; j < n_it; ++j) {
-          const bool more = j + 1 < n_it;
+          const bool more = j + 1 < n_it, last = last_of(j), first = PARTS > 1 ? j % kTaSegment == 0 : j == 0;
           const int sk = sv + 1 == ST ? 0 : sv + 1, pk = sv + 1 == ST ? ph ^ 1 : ph;
           if (!warp_wait(bar_full(sv), ph, stop)) return;
           if (more && !warp_wait(bar_full(sk), pk, stop)) return;
@@ -289,10 +294,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
 #pragma unroll
                   for (int part = 0; part < PARTS; ++part)
                     mma_ts(kO + t * D, t * 128 + part * (BN / 2) + ks * 8, c + (ks * 2048 >> 4), idesc_o,
-                           j > 0 || ks > 0 || part > 0);
+                           !first || ks > 0 || part > 0);
                 if (h == 1) {
+                  if (last) mma_commit(bar_o(t));
                   if (more) scores(t, sk);
-                  else mma_commit(bar_o(t));
                   if (t + 1 == tiles) {
                     mma_commit(bar_empty(sv));
                     if (more) mma_commit(bar_empty(sk));
@@ -324,6 +329,48 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     const uint32_t s_t = lanes + t * 128, o_t = lanes + kO + t * D;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
+    const int64_t row = (int64_t)(q0 + i0 + tok) * p.Hq + hd;
+    const bool part = PARTS > 1 || p.splits > 1;
+    int seg = 0;
+    auto part_row = [&]() {
+      return ((int64_t)blockIdx.y * (PARTS > 1 ? p.segments : 1) + seg) * p.total_q * p.Hq + row;
+    };
+    auto take_out = [&](bool have) {  // O and l of the row so far
+      const float inv = part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      const int64_t prow = part_row();
+      const bool room = PARTS == 1 || seg < p.segments;  // (a row longer than the cache's max_len has none)
+      if (part && valid && room)
+        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(l > 0.f ? m * sc : -INFINITY, l);
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (have) {
+          tmem_ld32(o, o_t + c);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (valid && part && room) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_acc + prow * D + c);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        } else if (valid && !part) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              v[u] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * u]) * inv, __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
+            dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+        __syncwarp();
+      }
+      ++seg;
+      l = 0.f;
+    };
     if (t < tiles) {
       for (int j = 0; j < n_it; ++j) {
         if (!(ok = warp_wait(bar_s(t), j & 1, stop))) break;
@@ -350,20 +397,44 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
             for (int c = 0; c < BN; ++c)
               if (c > hi || (c <= lo && c >= sk)) s[c] = 0xff800000u;
           }
-          // the first piece's weights with the m at hand, and the tile's maximum beside them: the maximum is
-          // off the path from scores to weights unless m has to change
-          float ms = 0.f;
-          uint64_t sum = 0;
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto weights = [&](auto& w, int c0, int n, bool with_max) {  // of tokens c0 .. c0 + 2 n - 1
-            const uint64_t ms2 = f2(ms, ms);
+#pragma unroll
+          for (int c = 0; c < BN; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool grow = (top - m) * sc > kTaGrowth;  // false while nothing has been seen
+          if (__any_sync(0xffffffffu, grow)) {
+            const float mn = grow ? top : m;
+            const float al = grow ? ex2((m - mn) * sc) : 1.f;
+            l *= al;
+            m = mn;
+            if (PARTS > 1 ? j % kTaSegment != 0 : j > 0) {
+              const uint64_t al2 = f2(al, al);
+#pragma unroll
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(o, o_t + c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float x, y;
+                  f2_split(f2_mul(f2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), x, y);
+                  o[e] = __float_as_uint(x);
+                  o[e + 1] = __float_as_uint(y);
+                }
+                tmem_st32(o_t + c, o);
+              }
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : -m * sc;
+          const uint64_t ms2 = f2(ms, ms);
+          uint64_t sum = 0;
+          auto weights = [&](auto& w, int c0, int n) {  // of tokens c0 .. c0 + 2 n - 1
 #pragma unroll
             for (int e = 0; e < n; ++e) {
               const int c = c0 + 2 * e;
-              if (with_max) {
-                mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                if (e < (BN - C0) / 2) mx[e & 3] = max3(mx[e & 3], __uint_as_float(s[C0 + 2 * e]), __uint_as_float(s[C0 + 2 * e + 1]));
-              }
               const uint64_t v2 = f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2);
               float x, y;
               if (PARTS == 1 && e % kTaPolyOf < kTaPoly) {
@@ -390,43 +461,14 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
             if (lane == 0) mbar_arrive(bar_p(t, h));
           };
           uint32_t w0[PARTS][C0 / 2];
-          if (m != -INFINITY) ms = -m * sc;
-          weights(w0, 0, C0 / 2, true);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool grow = (top - m) * sc > kTaGrowth;  // false while nothing has been seen
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? top : m;
-            const float al = grow ? ex2((m - mn) * sc) : 1.f;
-            l *= al;
-            m = mn;
-            if (j > 0) {
-              const uint64_t al2 = f2(al, al);
-#pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, o_t + c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  float x, y;
-                  f2_split(f2_mul(f2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), x, y);
-                  o[e] = __float_as_uint(x);
-                  o[e + 1] = __float_as_uint(y);
-                }
-                tmem_st32(o_t + c, o);
-              }
-            }
-            if (m != -INFINITY) ms = -m * sc;
-            sum = 0;
-            weights(w0, 0, C0 / 2, false);
-          }
+          weights(w0, 0, C0 / 2);
 #pragma unroll
           for (int part = 0; part < PARTS; ++part)
 #pragma unroll
             for (int c = 0; c < C0 / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + c, w0[part] + c);
           publish(0);
           uint32_t w1[PARTS][(BN - C0) / 2];
-          weights(w1, C0, (BN - C0) / 2, false);
+          weights(w1, C0, (BN - C0) / 2);
 #pragma unroll
           for (int part = 0; part < PARTS; ++part)
 #pragma unroll
@@ -435,52 +477,26 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
           float x, y;
           f2_split(sum, x, y);
           l += x + y;
-          continue;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane < 2) mbar_arrive(bar_p(t, lane));
-      }
-      if (ok && n_it > 0) ok = warp_wait(bar_o(t), 0, stop);
-      tc_fence_after();
-      if (ok && live) {
-        const int64_t row = (int64_t)(q0 + i0 + tok) * p.Hq + hd;
-        const bool part = p.splits > 1 || p.keep_partials;
-        const int64_t prow = (int64_t)blockIdx.y * p.total_q * p.Hq + row;
-        const float inv = part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-        if (part && valid) {
-          float* ml = p.part_ml + prow * 2;
-          ml[0] = l > 0.f ? m * sc : -INFINITY;
-          ml[1] = l;
-        }
-#pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (n_it > 0) {
-            tmem_ld32(o, o_t + c);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0;
-          }
-          if (valid && part) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_acc + prow * D + c);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          } else if (valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                w[u] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * u]) * inv, __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
+        if (!live || none) {
+          tc_fence_before();
           __syncwarp();
+          if (lane < 2) mbar_arrive(bar_p(t, lane));
+        }
+        if (PARTS > 1 && last_of(j)) {
+          if (!(ok = warp_wait(bar_o(t), (j / kTaSegment) & 1, stop))) break;
+          tc_fence_after();
+          if (live) take_out(true);
         }
       }
+      if (PARTS == 1 && n_it > 0) {
+        ok = ok && warp_wait(bar_o(t), 0, stop);
+        tc_fence_after();
+        if (ok && live) take_out(true);
+      }
+      if (n_it == 0 && live) take_out(false);
+      if (PARTS > 1 && valid)  // segments that this row did not need
+        for (; seg < p.segments; ++seg) *reinterpret_cast<float2*>(p.part_ml + part_row() * 2) = make_float2(-INFINITY, 0.f);
     }
   }
   __syncwarp();
@@ -497,7 +513,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   }
   __syncthreads();
   if (warp == 10) tmem_dealloc<512>(tmem);
-  grid_dep_wait();  // with late_wait: what follows this kernel relies on the one before it, too
 }
 
 // ---------------------------------------------------------------------- joining partial rows
@@ -513,40 +528,66 @@ struct MergeParams {
   uint8_t heads[kMaxHeads];
 };
 
-constexpr int kTmThreads = 128;
+constexpr int kTmThreads = 128, kTmFlight = 8;
 
-// One warp per (row, listed q head).  The partials are added in a fixed order.
+// One block per (row, listed q head): its warps take every fourth partial, lanes D / 32 dims each,
+// kTmFlight rows of partials in flight per warp; warps and partials are added in a fixed order.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParams p) {
   grid_dep_wait();
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * (kTmThreads / 32) + (threadIdx.x >> 5);
+  constexpr int E = D / 32, NW = kTmThreads / 32;
+  using Vec = typename std::conditional<E == 4, float4, float2>::type;
+  __shared__ float s_acc[NW][D], s_l[NW];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_row = p.n_listed * p.G;
-  const int64_t row = item / per_row;
-  const int hl = (int)(item % per_row), y = hl / p.G, h = p.heads[y] * p.G + hl % p.G;
-  if (row >= p.total_q) return;
+  const int row = (int)(blockIdx.x / per_row);
+  const int hl = (int)(blockIdx.x % per_row), y = hl / p.G, h = p.heads[y] * p.G + hl % p.G;
   bool tiles = true;
   if (p.q_offsets) {  // rows that no group holds have no tile partials
     tiles = row >= p.q_offsets[0] && row < p.q_offsets[p.B];
     if (!tiles && !p.own.pre) return;
-    if (!tiles && hl == 0 && lane == 0) record_error(kCheckPosition, (int)row, -1, p.B);
+    if (!tiles && hl == 0 && threadIdx.x == 0) record_error(kCheckPosition, row, -1, p.B);
   }
   const int ns = tiles ? p.splits : 0;
+  const int nv = p.own.NP + p.total_q;
   int no = 0, c0 = 0, c1 = 0;
-  if (p.own.pre && dense_row(p.own, p.n_listed, p.total_q, y, (int)row, &c0, &c1)) no = c1 - c0 + 1;
-  const int64_t rows = (int64_t)p.total_q * p.Hq, tr = row * p.Hq + h;
+  if (p.own.pre && dense_row(p.own, p.n_listed, nv, y, p.own.NP + row, &c0, &c1)) no = c1 - c0 + 1;
+  int np = 0, d0 = 0, d1 = 0, i = 0, first = 0;  // partials of the row's prefix in the dense pass
+  if (p.own.NP && tiles) {
+    if (p.q_offsets) {  // the prefix i whose range holds the row
+      int hi = p.B - 1;
+      while (i < hi) {
+        const int mid = (i + hi) >> 1;
+        if (p.q_offsets[mid + 1] > row) hi = mid; else i = mid + 1;
+      }
+      first = max(0, p.q_offsets[i]);
+    }
+    if (row >= first && (row - first + 1) * p.G <= p.own.nqp && dense_row(p.own, p.n_listed, nv, y, i, &d0, &d1))
+      np = d1 - d0 + 1;
+  }
+  const int64_t rows = (int64_t)p.total_q * p.Hq, tr = (int64_t)row * p.Hq + h;
+  // part s: of the tiles, of the row's own tokens, of its prefix; (m, l) and acc
+  auto dense_at = [&](int s, bool* whole) {
+    const bool own = s < ns + no;
+    const int a = own ? c0 : d0, e = own ? c1 : d1, v = own ? p.own.NP + row : i;
+    const int qr = own ? hl % p.G : (row - first) * p.G + hl % p.G;
+    *whole = a == e;
+    return (a == e ? (int64_t)y * nv + v : dense_part(a, s - ns - (own ? 0 : no))) * p.own.nqp + qr;
+  };
   auto ml_of = [&](int s) {
     if (s < ns) return p.part_ml + (s * rows + tr) * 2;
-    const int64_t r = c0 == c1 ? (int64_t)y * p.total_q + row : dense_part(c0, s - ns);
-    return (c0 == c1 ? p.own.row_ml : p.own.part_ml) + (r * p.own.nqp + hl % p.G) * 2;
+    bool whole;
+    const int64_t r = dense_at(s, &whole);
+    return (whole ? p.own.row_ml : p.own.part_ml) + r * 2;
   };
   auto acc_of = [&](int s) {
     if (s < ns) return p.part_acc + (s * rows + tr) * D;
-    if (c0 == c1) return static_cast<const float*>(p.out) + tr * D;
-    return p.own.part_acc + ((int64_t)dense_part(c0, s - ns) * p.own.nqp + hl % p.G) * D;
+    bool whole;
+    const int64_t r = dense_at(s, &whole);
+    if (!whole) return p.own.part_acc + r * D;
+    return p.own.packed ? p.own.row_acc + r * D : p.own.row_acc + tr * D;
   };
-  const int nt = ns + no;
+  const int nt = ns + no + np;
   float M = -INFINITY;
   for (int s = lane; s < nt; s += 32) M = fmaxf(M, ml_of(s)[0]);
 #pragma unroll
@@ -554,24 +595,47 @@ __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParam
   float acc[E], l = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < nt; ++s) {
-    const float* ml = ml_of(s);
-    const float* a = acc_of(s) + lane * E;
-    const float w = ml[0] == -INFINITY ? 0.f : exp2f(ml[0] - M);
-    l += w * ml[1];
+  for (int s0 = warp; s0 < nt; s0 += NW * kTmFlight) {
+    Vec v[kTmFlight];
+    float2 ml[kTmFlight];
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = w > 0.f ? fmaf(w, a[e], acc[e]) : acc[e];
+    for (int k = 0; k < kTmFlight; ++k) {
+      const int s = s0 + k * NW;
+      if (s < nt) {
+        ml[k] = *reinterpret_cast<const float2*>(ml_of(s));
+        v[k] = *reinterpret_cast<const Vec*>(acc_of(s) + lane * E);
+      } else {
+        ml[k] = make_float2(-INFINITY, 0.f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kTmFlight; ++k) {
+      if (ml[k].x == -INFINITY) continue;  // nothing seen: its acc may never have been written
+      const float w = ex2(ml[k].x - M);
+      const float* a = reinterpret_cast<const float*>(&v[k]);
+      l = fmaf(w, ml[k].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, a[e], acc[e]);
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  if (BF16) {
-    uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + tr * D + lane * E);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  } else {
-    float* o = static_cast<float*>(p.out) + tr * D + lane * E;
+  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  if (threadIdx.x < D / 2) {
+    const int d = 2 * threadIdx.x;
+    float a = 0.f, b = 0.f, t = 0.f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = acc[e] * inv;
+    for (int w = 0; w < NW; ++w) {
+      a += s_acc[w][d];
+      b += s_acc[w][d + 1];
+      t += s_l[w];
+    }
+    const float inv = t > 0.f ? 1.f / t : 0.f;
+    if (BF16)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + tr * D + d) = pack_bf16x2(a * inv, b * inv);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + tr * D + d) = make_float2(a * inv, b * inv);
   }
 }
 
