@@ -1975,13 +1975,13 @@ int list_by_role(const aoh_kv_cache* kv, const uint8_t* roles, uint8_t* out) {
 }
 
 struct TileWs {
-  int slots, splits, segments;
+  int slots, splits;
   size_t off_acc, total;
 };
 
 // The grid of a tile call: a slot per two tiles of rows of every group, times the heads, times as
-// many splits of the key range as give every SM a CTA, of at least four key tiles each, or, where every
-// split leaves partials anyway, of a partial's (64 sequences behind 8192 tokens, with the pass over their
+// many splits of the key range as give every SM a CTA, of at least four key tiles each, or sixteen where every
+// split leaves partials anyway (64 sequences behind 8192 tokens, with the pass over their
 // own tokens on the other SMs: 18 splits 77 us, 10 68 us, 8 66 us).
 TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, const uint8_t* roles, int32_t sink,
                int32_t window, int bn, bool keep) {
@@ -1998,12 +1998,9 @@ TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, 
     longest = std::max(longest, r == AOH_ROLE_DENSE ? L : std::min<int64_t>(L, int64_t(sink) + window + P2));
   }
   const int64_t ctas = std::max<int64_t>(1, int64_t(w.slots) * n_listed);
-  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count() / ctas, ceil_div(longest, bn) / (keep ? kTaSegment : 4)));
-  // (a bound for the tiles of a split: a key range's share, rounded up)
-  w.segments = keep ? (int)ceil_div(ceil_div(ceil_div(longest, bn), w.splits), kTaSegment) : 1;
-  w.segments = std::max(w.segments, 1);
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count() / ctas, ceil_div(longest, bn) / (keep ? kTaSplitTiles : 4)));
   if (w.splits > 1 || keep) {
-    const size_t rows = (size_t)w.splits * w.segments * (size_t)total_q * Hq;
+    const size_t rows = (size_t)w.splits * (size_t)ctas * 2 * 128;  // whole tiles
     w.off_acc = align256(sizeof(float) * 2 * rows);
     w.total = w.off_acc + align256(sizeof(float) * rows * kv->head_dim);
   }
@@ -2018,15 +2015,15 @@ aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_ca
   tp.offsets = kv->offsets;
   bind_cache(tp, kv);
   tp.q_offsets = q_offsets;
-  tp.part_ml = static_cast<float*>(workspace);
-  tp.part_acc = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.off_acc);
+  tp.part_ml = static_cast<float2*>(workspace);
+  tp.part_acc = reinterpret_cast<float4*>(static_cast<uint8_t*>(workspace) + w.off_acc);
   tp.B = kv->batch;
   tp.Hq = Hq;
   tp.G = G;
   tp.PT = PT;
   tp.total_q = (int)total_q;
   tp.splits = w.splits;
-  tp.segments = w.segments;
+  tp.slots = w.slots;
   // a positive factor: masked scores are -inf before they are scaled, and -inf * 0 is a NaN
   tp.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);
   tp.neg = scale < 0.f;
@@ -2051,7 +2048,9 @@ aoh_status launch_tiles(TileParams& tp, const TileWs& w, int n_listed, cudaStrea
   return launch_dependent(kern, dim3((unsigned)(int64_t(w.slots) * n_listed), w.splits), kTaThreads, smem, 0, st, tp);
 }
 
-void bind_merge(MergeParams& mp, const TileParams& tp, int n_listed, void* out) {
+void bind_merge(MergeParams& mp, const TileParams& tp, const TileWs& w, int n_listed, void* out) {
+  mp.PT = tp.PT;
+  mp.slots = w.slots;
   mp.part_ml = tp.part_ml;
   mp.part_acc = tp.part_acc;
   mp.q_offsets = tp.q_offsets;
@@ -2060,15 +2059,15 @@ void bind_merge(MergeParams& mp, const TileParams& tp, int n_listed, void* out) 
   mp.Hq = tp.Hq;
   mp.G = tp.G;
   mp.total_q = tp.total_q;
-  mp.splits = tp.splits * tp.segments;
+  mp.splits = tp.splits;
   mp.n_listed = n_listed;
   memcpy(mp.heads, tp.heads, sizeof(mp.heads));
 }
 
 template <int D, bool BF16>
 aoh_status launch_merge(const MergeParams& mp, cudaStream_t st) {
-  const int64_t blocks = int64_t(mp.total_q) * mp.n_listed * mp.G;
-  aoh_status s = launch_dependent(tile_merge_kernel<D, BF16>, dim3((unsigned)blocks), kTmThreads, 0, 0, st, mp);
+  const int64_t blocks = ceil_div(int64_t(mp.total_q) * mp.G, 32);
+  aoh_status s = launch_dependent(tile_merge_kernel<D, BF16>, dim3((unsigned)blocks, mp.n_listed), kTmThreads, 0, 0, st, mp);
   return s != AOH_OK ? s : count_launch(AOH_KERNEL_TILE_MERGE, st);
 }
 
@@ -2172,7 +2171,7 @@ aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cac
   s = kv->head_dim == 128 ? launch_tiles<128, 1>(tp, w, n_listed, st) : launch_tiles<64, 1>(tp, w, n_listed, st);
   if (s != AOH_OK || (s = count_launch(AOH_KERNEL_TILE_ATTEND, st)) != AOH_OK || w.splits == 1) return s;
   MergeParams mp{};
-  bind_merge(mp, tp, n_listed, out);
+  bind_merge(mp, tp, w, n_listed, out);
   return kv->head_dim == 128 ? launch_merge<128, true>(mp, st) : launch_merge<64, true>(mp, st);
 }
 
@@ -2209,6 +2208,7 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
     mp.B = prefix->batch;
     mp.Hq = n_q_heads;
     mp.G = n_q_heads / kv->n_kv_heads;
+    mp.PT = 128 / mp.G;
     mp.total_q = kv->batch;
     mp.n_listed = n_listed;
     memcpy(mp.heads, heads, sizeof(mp.heads));
@@ -2226,7 +2226,7 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
   // the sequences' own tokens, beside the tiles on SMs that these leave; what one CTA finishes of them
   // waits in out for the merge
   if ((s = launch_dense(q, n_q_heads, kv, scale, out, false, nullptr, 0, true, w.own, ws, &mp.own, st)) != AOH_OK) return s;
-  bind_merge(mp, tp, n_listed, out);
+  bind_merge(mp, tp, w.tiles, n_listed, out);
   return kv->head_dim == 128 ? launch_merge<128, false>(mp, st) : launch_merge<64, false>(mp, st);
 }
 

@@ -28,8 +28,8 @@
 // rounding of a bf16 output); PARTS = 3, for fp32 outputs, keeps 24 bits as three bf16 terms, each
 // multiplied with V (two terms and key tiles of 128 were a tenth faster and twice as far off).  The
 // accumulation in TMEM drops the bits below the accumulator's last, always towards zero, which adds
-// up along a row (9e-6 after 3600 tokens): with PARTS = 3 a row's O is therefore taken out as a partial
-// of its own after every kTaSegment key tiles.
+// up along a row (9e-6 after 3600 tokens): with PARTS = 3 a row's O is therefore added to its partial in
+// memory (which stays in L2) after every kTaSegment key tiles, and begins again from zero.
 #pragma once
 
 #include <type_traits>
@@ -43,7 +43,9 @@ constexpr int kTaRegsSoftmax = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 re
 constexpr int kTaRegsOther = 88;
 constexpr int kTaRegsLaunch = 168;
 constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
-constexpr int kTaSegment = 16;        // key tiles of a partial (PARTS > 1)
+constexpr int kTaSegment = 8;         // key tiles that O gathers (PARTS > 1; 16: 150 us instead of 160 for 96
+                                      // sequences behind two documents, and half as exact again)
+constexpr int kTaSplitTiles = 16;     // key tiles of a split at least, where every split leaves partials
 constexpr float kTaGrowth = 60.f;     // log2 of the largest weight before a rescale
 
 template <int D, int PARTS>
@@ -64,10 +66,10 @@ struct alignas(64) TileParams {
   const int32_t* lengths;    // [B] or null
   const int32_t* q_offsets;  // [B + 1] rows of every group, or null: one group of all rows
   uint16_t* out;             // splits == 1: bf16 [total_q][Hq][D]
-  float* part_ml;            // else (m, l) [splits][segments][total_q][Hq][2], m times scale_log2
-  float* part_acc;           //      [splits][segments][total_q][Hq][D]
-  int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed;
-  int32_t segments;          // partials of a split (PARTS > 1)
+  // else partials per (split, tile of rows): rows are the fastest index, a row per lane
+  float2* part_ml;           // (m, l) [splits][tiles][128], m times scale_log2
+  float4* part_acc;          // [splits][tiles][D / 4][128]
+  int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed, slots;
   int32_t causal;            // 0: every row sees the whole group
   float scale_log2;          // > 0; a negative scale negates Q in the product
   uint32_t neg;
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   } else {  // ---------------------------------------------------------------------- softmax of tile wg
     regs_inc<kTaRegsSoftmax>();
     const int t = wg, r = tid & 127, wr = r & ~31;
-    const int tok = t * PT + r / p.G, hd = g * p.G + r % p.G;
+    const int tok = t * PT + r / p.G;
     const bool valid = r < PT * p.G && tok < np;
     const bool live = t < tiles && wr < PT * p.G && t * PT + wr / p.G < np;  // some row of the warp exists
     const int pos = p.causal ? max(L - n + i0 + tok, -1) : L - 1;
@@ -329,18 +331,17 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     const uint32_t s_t = lanes + t * 128, o_t = lanes + kO + t * D;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    const int64_t row = (int64_t)(q0 + i0 + tok) * p.Hq + hd;
     const bool part = PARTS > 1 || p.splits > 1;
-    int seg = 0;
-    auto part_row = [&]() {
-      return ((int64_t)blockIdx.y * (PARTS > 1 ? p.segments : 1) + seg) * p.total_q * p.Hq + row;
-    };
-    auto take_out = [&](bool have) {  // O and l of the row so far
+    float fac = 1.f;  // what the row's partial in memory is still to be scaled by
+    auto take_out = [&](bool have, bool add) {  // O and l of the row; add: to the partial written before
       const float inv = part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
-      const int64_t prow = part_row();
-      const bool room = PARTS == 1 || seg < p.segments;  // (a row longer than the cache's max_len has none)
-      if (part && valid && room)
-        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(l > 0.f ? m * sc : -INFINITY, l);
+      const int64_t pt = ((int64_t)blockIdx.y * p.slots * p.n_listed + (int64_t)slot_id * p.n_listed + y) * 2 + t;
+      float4* acc_out = p.part_acc + pt * (D / 4) * 128 + r;
+      if (part) p.part_ml[pt * 128 + r] = make_float2(valid && l > 0.f ? m * sc : -INFINITY, l);
+      // A finished row goes through the warp's rows of Q in shared memory (no product reads Q any more),
+      // 16-byte pieces XOR-swizzled, so that whole rows leave in full lines.
+      const uint32_t stage = q_s + t * T::kQBytes + wr * (D * 2);
+      auto piece = [&](int rr, int ch) { return stage + rr * (D * 2) + ((ch ^ (rr & 7)) << 4); };
 #pragma unroll
       for (int c = 0; c < D; c += 32) {
         uint32_t o[32];
@@ -351,25 +352,52 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (valid && part && room) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_acc + prow * D + c);
+        if (part) {
+          float4 old[8];
+          if (PARTS > 1 && add)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-        } else if (valid && !part) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + c);
+            for (int e = 0; e < 8; ++e) old[e] = __ldcg(acc_out + (c / 4 + e) * 128);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float4 v = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
+                                   __uint_as_float(o[4 * e + 3]));
+            if (PARTS > 1 && add) {
+              v.x = fmaf(old[e].x, fac, v.x);
+              v.y = fmaf(old[e].y, fac, v.y);
+              v.z = fmaf(old[e].z, fac, v.z);
+              v.w = fmaf(old[e].w, fac, v.w);
+            }
+            __stcg(acc_out + (c / 4 + e) * 128, v);
+          }
+        } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               v[u] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * u]) * inv, __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
-            dst[e] = make_uint4(v[0], v[1], v[2], v[3]);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(piece(lane, c / 8 + e)), "r"(v[0]), "r"(v[1]),
+                         "r"(v[2]), "r"(v[3])
+                         : "memory");
           }
         }
-        __syncwarp();
       }
-      ++seg;
-      l = 0.f;
+      __syncwarp();
+      if (!part) {
+        constexpr int LPR = D / 8;  // lanes per row
+#pragma unroll 4
+        for (int k = 0; k < LPR; ++k) {
+          const int rr = k * (32 / LPR) + lane / LPR, ch = lane % LPR, rw = wr + rr;
+          const int tk = t * PT + rw / p.G;
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(piece(rr, ch)));
+          if (rw < PT * p.G && tk < np)
+            *reinterpret_cast<uint4*>(p.out + ((int64_t)(q0 + i0 + tk) * p.Hq + g * p.G + rw % p.G) * D + ch * 8) = v;
+        }
+      }
+      fac = 1.f;
     };
     if (t < tiles) {
       for (int j = 0; j < n_it; ++j) {
@@ -409,6 +437,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
             const float mn = grow ? top : m;
             const float al = grow ? ex2((m - mn) * sc) : 1.f;
             l *= al;
+            fac *= al;
             m = mn;
             if (PARTS > 1 ? j % kTaSegment != 0 : j > 0) {
               const uint64_t al2 = f2(al, al);
@@ -486,17 +515,15 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
         if (PARTS > 1 && last_of(j)) {
           if (!(ok = warp_wait(bar_o(t), (j / kTaSegment) & 1, stop))) break;
           tc_fence_after();
-          if (live) take_out(true);
+          if (live) take_out(true, j >= kTaSegment);
         }
       }
       if (PARTS == 1 && n_it > 0) {
         ok = ok && warp_wait(bar_o(t), 0, stop);
         tc_fence_after();
-        if (ok && live) take_out(true);
+        if (ok && live) take_out(true, false);
       }
-      if (n_it == 0 && live) take_out(false);
-      if (PARTS > 1 && valid)  // segments that this row did not need
-        for (; seg < p.segments; ++seg) *reinterpret_cast<float2*>(p.part_ml + part_row() * 2) = make_float2(-INFINITY, 0.f);
+      if (n_it == 0 && live) take_out(false, false);
     }
   }
   __syncwarp();
@@ -517,125 +544,127 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
 
 // ---------------------------------------------------------------------- joining partial rows
 struct MergeParams {
-  const float* part_ml;      // tile partials [splits][rows][Hq] ...
-  const float* part_acc;
+  const float2* part_ml;     // tile partials, `splits` of every tile of rows
+  const float4* part_acc;
   const int32_t* q_offsets;  // rows of every group ([B + 1]) or null: one group of all rows
   void* out;                 // bf16 or fp32 [total_q][Hq][D]
-  int32_t B, Hq, G, total_q, splits, n_listed;
-  // the rows' own tokens (row b is sequence b), or no own.pre; what one CTA finished is in out, not
-  // divided by its sum
+  int32_t B, Hq, G, PT, total_q, splits, n_listed, slots;
+  // the rows' own tokens (row b is sequence b) and, with own.NP, its prefix, or no own.pre; without
+  // own.packed what one CTA finished is in out, not divided by its sum
   DenseRows own;
   uint8_t heads[kMaxHeads];
 };
 
-constexpr int kTmThreads = 128, kTmFlight = 8;
+constexpr int kTmThreads = 256, kTmFlight = 4;
 
-// One block per (row, listed q head): its warps take every fourth partial, lanes D / 32 dims each,
-// kTmFlight rows of partials in flight per warp; warps and partials are added in a fixed order.
+// grid (32 (row, q head of the group) pairs, listed heads): a pair per lane, so that the partials of a
+// tile are read as they were written; warps share the D / 4 pieces of the rows.  Partials are added in
+// a fixed order.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParams p) {
   grid_dep_wait();
-  constexpr int E = D / 32, NW = kTmThreads / 32;
-  using Vec = typename std::conditional<E == 4, float4, float2>::type;
-  __shared__ float s_acc[NW][D], s_l[NW];
+  constexpr int NC = D / 4 / (kTmThreads / 32);  // pieces of a warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_row = p.n_listed * p.G;
-  const int row = (int)(blockIdx.x / per_row);
-  const int hl = (int)(blockIdx.x % per_row), y = hl / p.G, h = p.heads[y] * p.G + hl % p.G;
+  const int64_t item = (int64_t)blockIdx.x * 32 + lane;
+  const int row = (int)(item / p.G), hq = (int)(item % p.G), y = blockIdx.y, h = p.heads[y] * p.G + hq;
+  if (row >= p.total_q) return;
   bool tiles = true;
-  if (p.q_offsets) {  // rows that no group holds have no tile partials
-    tiles = row >= p.q_offsets[0] && row < p.q_offsets[p.B];
+  int i = 0, first = 0;  // the row's group and its first row
+  if (p.q_offsets) {
+    tiles = row >= p.q_offsets[0] && row < p.q_offsets[p.B];  // rows that no group holds have no tile partials
     if (!tiles && !p.own.pre) return;
-    if (!tiles && hl == 0 && threadIdx.x == 0) record_error(kCheckPosition, row, -1, p.B);
+    if (!tiles && y == 0 && hq == 0 && warp == 0) record_error(kCheckPosition, row, -1, p.B);
+    int hi = p.B - 1;
+    while (i < hi) {
+      const int mid = (i + hi) >> 1;
+      if (p.q_offsets[mid + 1] > row) hi = mid; else i = mid + 1;
+    }
+    first = max(0, p.q_offsets[i]);
+    tiles = tiles && row >= first;
   }
-  const int ns = tiles ? p.splits : 0;
+  const int P2 = 2 * p.PT, rel = row - first;
+  const int64_t slot = p.q_offsets ? ((int64_t)first + (int64_t)i * (P2 - 1)) / P2 + rel / P2 : rel / P2;
+  const int64_t n_tiles = (int64_t)p.slots * p.n_listed * 2, u = (slot * p.n_listed + y) * 2 + (rel % P2) / p.PT;
+  const int rr = (rel % p.PT) * p.G + hq;
+  const int ns = tiles && slot < p.slots ? p.splits : 0;
   const int nv = p.own.NP + p.total_q;
   int no = 0, c0 = 0, c1 = 0;
   if (p.own.pre && dense_row(p.own, p.n_listed, nv, y, p.own.NP + row, &c0, &c1)) no = c1 - c0 + 1;
-  int np = 0, d0 = 0, d1 = 0, i = 0, first = 0;  // partials of the row's prefix in the dense pass
-  if (p.own.NP && tiles) {
-    if (p.q_offsets) {  // the prefix i whose range holds the row
-      int hi = p.B - 1;
-      while (i < hi) {
-        const int mid = (i + hi) >> 1;
-        if (p.q_offsets[mid + 1] > row) hi = mid; else i = mid + 1;
-      }
-      first = max(0, p.q_offsets[i]);
-    }
-    if (row >= first && (row - first + 1) * p.G <= p.own.nqp && dense_row(p.own, p.n_listed, nv, y, i, &d0, &d1))
-      np = d1 - d0 + 1;
-  }
-  const int64_t rows = (int64_t)p.total_q * p.Hq, tr = (int64_t)row * p.Hq + h;
-  // part s: of the tiles, of the row's own tokens, of its prefix; (m, l) and acc
+  int np = 0, d0 = 0, d1 = 0;  // partials of the row's prefix in the dense pass
+  if (p.own.NP && tiles && (rel + 1) * p.G <= p.own.nqp && dense_row(p.own, p.n_listed, nv, y, i, &d0, &d1)) np = d1 - d0 + 1;
+  const int64_t tr = (int64_t)row * p.Hq + h;
+  // part s: of the tiles, of the row's own tokens, of its prefix
   auto dense_at = [&](int s, bool* whole) {
     const bool own = s < ns + no;
     const int a = own ? c0 : d0, e = own ? c1 : d1, v = own ? p.own.NP + row : i;
-    const int qr = own ? hl % p.G : (row - first) * p.G + hl % p.G;
     *whole = a == e;
-    return (a == e ? (int64_t)y * nv + v : dense_part(a, s - ns - (own ? 0 : no))) * p.own.nqp + qr;
+    return (a == e ? (int64_t)y * nv + v : dense_part(a, s - ns - (own ? 0 : no))) * p.own.nqp +
+           (own ? hq : rel * p.G + hq);
   };
   auto ml_of = [&](int s) {
-    if (s < ns) return p.part_ml + (s * rows + tr) * 2;
+    if (s < ns) return p.part_ml[(s * n_tiles + u) * 128 + rr];
     bool whole;
     const int64_t r = dense_at(s, &whole);
-    return (whole ? p.own.row_ml : p.own.part_ml) + r * 2;
+    return *reinterpret_cast<const float2*>((whole ? p.own.row_ml : p.own.part_ml) + r * 2);
   };
-  auto acc_of = [&](int s) {
-    if (s < ns) return p.part_acc + (s * rows + tr) * D;
+  auto acc_of = [&](int s, int64_t* step) {  // first piece and the distance of the next, in float4
+    if (s < ns) {
+      *step = 128;
+      return p.part_acc + (s * n_tiles + u) * (D / 4) * 128 + rr;
+    }
     bool whole;
     const int64_t r = dense_at(s, &whole);
-    if (!whole) return p.own.part_acc + r * D;
-    return p.own.packed ? p.own.row_acc + r * D : p.own.row_acc + tr * D;
+    *step = 1;
+    const float* a = !whole ? p.own.part_acc + r * D : p.own.packed ? p.own.row_acc + r * D : p.own.row_acc + tr * D;
+    return reinterpret_cast<const float4*>(a);
   };
   const int nt = ns + no + np;
   float M = -INFINITY;
-  for (int s = lane; s < nt; s += 32) M = fmaxf(M, ml_of(s)[0]);
+#pragma unroll 4
+  for (int s = 0; s < nt; ++s) M = fmaxf(M, ml_of(s).x);
+  float4 acc[NC];
+  float l = 0.f;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float acc[E], l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s0 = warp; s0 < nt; s0 += NW * kTmFlight) {
-    Vec v[kTmFlight];
+  for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < nt; s0 += kTmFlight) {
+    float4 v[kTmFlight][NC];
     float2 ml[kTmFlight];
 #pragma unroll
     for (int k = 0; k < kTmFlight; ++k) {
-      const int s = s0 + k * NW;
-      if (s < nt) {
-        ml[k] = *reinterpret_cast<const float2*>(ml_of(s));
-        v[k] = *reinterpret_cast<const Vec*>(acc_of(s) + lane * E);
-      } else {
-        ml[k] = make_float2(-INFINITY, 0.f);
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (s0 + k < nt) {
+        ml[k] = ml_of(s0 + k);
+        int64_t step;
+        const float4* a = acc_of(s0 + k, &step);
+        if (ml[k].x != -INFINITY)  // else nothing was seen, and its acc may never have been written
+#pragma unroll
+          for (int c = 0; c < NC; ++c) v[k][c] = a[(warp * NC + c) * step];
       }
     }
 #pragma unroll
     for (int k = 0; k < kTmFlight; ++k) {
-      if (ml[k].x == -INFINITY) continue;  // nothing seen: its acc may never have been written
+      if (ml[k].x == -INFINITY) continue;
       const float w = ex2(ml[k].x - M);
-      const float* a = reinterpret_cast<const float*>(&v[k]);
       l = fmaf(w, ml[k].y, l);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, a[e], acc[e]);
+      for (int c = 0; c < NC; ++c) {
+        acc[c].x = fmaf(w, v[k][c].x, acc[c].x);
+        acc[c].y = fmaf(w, v[k][c].y, acc[c].y);
+        acc[c].z = fmaf(w, v[k][c].z, acc[c].z);
+        acc[c].w = fmaf(w, v[k][c].w, acc[c].w);
+      }
     }
   }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  if (threadIdx.x < D / 2) {
-    const int d = 2 * threadIdx.x;
-    float a = 0.f, b = 0.f, t = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      a += s_acc[w][d];
-      b += s_acc[w][d + 1];
-      t += s_l[w];
-    }
-    const float inv = t > 0.f ? 1.f / t : 0.f;
+  for (int c = 0; c < NC; ++c) {
+    const int d = (warp * NC + c) * 4;
     if (BF16)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + tr * D + d) = pack_bf16x2(a * inv, b * inv);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tr * D + d) =
+          make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
     else
-      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + tr * D + d) = make_float2(a * inv, b * inv);
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + tr * D + d) =
+          make_float4(acc[c].x * inv, acc[c].y * inv, acc[c].z * inv, acc[c].w * inv);
   }
 }
 
