@@ -452,6 +452,17 @@ def test_evict_layouts_slots_and_long_rows(d):
     check_evict(c, mass, 2048, 4, 512, res)
 
 
+def test_evict_rows_too_long_for_a_cluster():
+    # more than 131072 positions: the scores go through memory
+    c = Cache(165, [140000, 50], 1, 64)
+    mass = draw_mass(166, 1, c.T, "ties")
+    res = []
+    got = launches_of(lambda: res.append(run_evict(c, mass, 3000, 4, 100, 3000)))
+    check_device()
+    assert got["evict_key_kernel"] == 2 and got["evict_copy_kernel"] == 2
+    check_evict(c, mass, 3000, 4, 100, res[0])
+
+
 def test_evict_records_a_region_too_small():
     c = Cache(171, [10, 100, 20], 2, 64)
     mass = draw_mass(172, 2, c.T, "plain")
@@ -478,7 +489,7 @@ def test_steps_launch_the_kernels():
     d = Cache(183, [128, 128], 2, 128)
     ev = EvictStep(c.k, c.v, c.offsets, c.max_len, c.T, d.k, d.v, d.offsets, 128, d.T, 128, 4, 16)
     got = launches_of(lambda: ev(torch.rand((2, c.T), device="cuda"), None, d.lengths))
-    assert got.pop("evict_key_kernel") == 1 and got.pop("evict_copy_kernel") == 1
+    assert got == {"select_cluster_kernel": 1, "evict_copy_kernel": 1}
     pfx = PrefixDecodeStep(c.k, c.v, c.offsets[:2], 700, 700, d.k, d.v, d.offsets, 128, d.T, 8, 0.1)
     assert launches_of(lambda: pfx(q)) == {"dense_pass_kernel": 1, "tile_merge_kernel": 1}  # few rows: one pass
     many = Cache(185, [30] * 9, 2, 128)

@@ -7,18 +7,15 @@
 //     K'[j] = K[idx[j]],  V'[j] = V[idx[j]],  mass'[j] = mass[idx[j]],   j < n,
 // and lengths'[b] = n.  Each KV head keeps positions of its own, all heads equally many.
 //
-//   evict_key_kernel   writes the selection's scores: +inf for the protected positions, else
-//                      the weight, limited to the finite range (a NaN counts as the lightest)
-//                      so that a protected position always comes first;
-//   the exact top-n select of the library on those scores (ascending positions);
+//   select_cluster_kernel<true>  (rows up to 131072 positions) the exact top-n select on the weights,
+//                      keys in registers: protected positions count as +inf, a NaN as the lightest;
+//   evict_key_kernel and the library's select (longer rows): the same with the keys in memory;
 //   evict_copy_kernel  moves the rows.
 // All of it is bound by memory: 4 bytes per (head, position) for the weights and 8 d + 8 per
 // kept row read and written once.
 #pragma once
 
-#include <float.h>
-
-#include "device_common.cuh"
+#include "select_cluster.cuh"
 
 namespace aoh {
 
@@ -64,9 +61,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_key_kernel(const EvictPar
   for (int i = 0; i < 4; ++i) {
     const int pos = p0 + i * kEvictThreads + threadIdx.x;
     if (pos < L) {
-      const float m = src[pos];
-      const float lim = m != m ? -INFINITY : fminf(m, FLT_MAX);
-      dst[pos] = (pos < p.sink || pos >= L - p.recent) ? INFINITY : lim;
+      dst[pos] = evict_score(src[pos], pos, L, p.sink, p.recent);
     }
   }
 }

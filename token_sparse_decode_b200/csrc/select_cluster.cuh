@@ -23,6 +23,7 @@
 #pragma once
 
 #include <cooperative_groups.h>
+#include <float.h>
 
 #include "device_common.cuh"
 
@@ -42,9 +43,18 @@ struct ClusterSelectParams {
   int32_t* idx;                  // [B][Hkv][cap]
   int32_t* count;                // [B][Hkv]
   int32_t T, Hkv, n_fac, cap;
+  int32_t sink, recent;          // EVICT: positions taken before all others at either end
   uint8_t heads[kMaxHeads];      // KV head of blockIdx.y
 };
 
+// EVICT: the scores are accumulated attention weights; the first `sink` and the last `recent` positions come
+// before all others (+inf), and the others' weights are limited to the finite range (a NaN is the lightest).
+__device__ __forceinline__ float evict_score(float m, int pos, int L, int sink, int recent) {
+  const float lim = m != m ? -INFINITY : fminf(m, FLT_MAX);
+  return (pos < sink || pos >= L - recent) ? INFINITY : lim;
+}
+
+template <bool EVICT>
 __global__ void __launch_bounds__(kScThreads) select_cluster_kernel(const ClusterSelectParams p) {
   grid_dep_wait();  // the scores come from the kernel before this one
   grid_dep_launch();
@@ -90,7 +100,14 @@ __global__ void __launch_bounds__(kScThreads) select_cluster_kernel(const Cluste
   const float* row = p.scores + (int64_t)g * p.T + off;
   uint32_t k[kScK];
 #pragma unroll
-  for (int r = 0; r < kScK; ++r) k[r] = r * 32 + lane < nv ? score_key(__ldcg(row + w0 + r * 32 + lane)) : 0u;
+  for (int r = 0; r < kScK; ++r) {
+    k[r] = 0u;
+    if (r * 32 + lane < nv) {
+      float s = __ldcg(row + w0 + r * 32 + lane);
+      if (EVICT) s = evict_score(s, w0 + r * 32 + lane, L, p.sink, p.recent);
+      k[r] = score_key(s);
+    }
+  }
   __syncthreads();  // lh is zero
 
   uint32_t prefix = 0u, pmask = 0u;
