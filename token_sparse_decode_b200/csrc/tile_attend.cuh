@@ -80,28 +80,31 @@ struct alignas(64) TileParams {
 
 // The group and first row of CTA `slot`: group b's tiles of P2 rows take the slots from
 // floor((q_offsets[b] + b (P2 - 1)) / P2) on, room for ceil(n_b / P2) of them.
-__device__ __forceinline__ bool ta_locate(const TileParams& p, int slot, int* b_out, int* i0, int* n_out, int* q0_out) {
+struct TaPlace {
+  int b, i0, n, q0, off, L;
+};
+__device__ __forceinline__ bool ta_locate(const TileParams& p, int slot, TaPlace* w) {
   const int P2 = 2 * p.PT;
-  int b = 0, q0 = 0, q1 = p.total_q, s0 = 0;
+  int lo = 0, hi = p.B - 1, s0 = 0, q1 = p.total_q;
+  w->q0 = 0;
   if (p.q_offsets) {
-    int lo = 0, hi = p.B - 1;
     auto first = [&](int i) { return (int)(((int64_t)p.q_offsets[i] + (int64_t)i * (P2 - 1)) / P2); };
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (first(mid) <= slot) lo = mid; else hi = mid - 1;
     }
-    b = lo;
-    q0 = p.q_offsets[b];
-    q1 = p.q_offsets[b + 1];
-    s0 = first(b);
+    w->q0 = p.q_offsets[lo];
+    q1 = p.q_offsets[lo + 1];
+    s0 = first(lo);
+  } else {
+    lo = 0;
   }
-  const int n = q1 - q0;
+  w->b = lo;
+  w->L = seq_length(p.offsets, p.lengths, lo, false, &w->off);
+  w->n = q1 - w->q0;
   const int64_t i = (int64_t)(slot - s0) * P2;
-  *b_out = b;
-  *i0 = (int)i;
-  *n_out = n;
-  *q0_out = q0;
-  return q0 >= 0 && i >= 0 && i < n;
+  w->i0 = (int)i;
+  return w->q0 >= 0 && i >= 0 && i < w->n && w->q0 + i < p.total_q;  // (rows past those of q are recorded)
 }
 
 // 2^x of two numbers without the special-function unit, x <= 8: x = i + f with |f| <= 1/2 (i by adding
@@ -153,41 +156,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const uint32_t bar_q = bars + 8 * (2 * ST + 8), bar_fix = bars + 8 * (2 * ST + 9);
   const uint32_t bar_end = bars + 8 * (2 * ST + 10);
 
-  grid_dep_wait();
-  grid_dep_launch();
-  if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y) == 0 && p.q_offsets[p.B] > p.total_q)
-    record_error(kCheckPosition, p.B, p.q_offsets[p.B], p.total_q);  // rows past those of q are skipped
-  int b, i0, n, q0;
-  // later rows first, all heads of a tile together: the longest rows start first
-  const int slot_id = (int)((gridDim.x - 1 - blockIdx.x) / p.n_listed), y = (int)(blockIdx.x % p.n_listed);
-  if (!ta_locate(p, slot_id, &b, &i0, &n, &q0)) return;
-  if (q0 + i0 >= p.total_q) return;  // (recorded above)
-  const int g = p.heads[y];
-  const bool dense = p.roles[g] == 1;
-  int off;
-  const int L = seq_length(p.offsets, p.lengths, b, false, &off);
-  const int PT = p.PT;
-  // tokens of this CTA (one minimum of a difference: min(min(2 PT, n - i0), total_q - q0 - i0) came out of
-  // nvcc 12.9 without its second term)
-  const int row_end = min(q0 + n, p.total_q), np = min(row_end - (q0 + i0), 2 * PT);
-  const int tiles = np > PT ? 2 : 1;
-  // key tiles that some row sees: [0, a1) and [b0, b1)
-  const int p_lo = p.causal ? max(L - n + i0, -1) : L - 1;
-  const int p_hi = p.causal ? max(L - n + i0 + np - 1, -1) : L - 1;
-  int a1 = 0, b0 = 0;
-  const int b1 = (p_hi + BN) / BN;  // ceil((p_hi + 1) / BN)
-  if (!dense) {
-    a1 = (min(p.sink, p_hi + 1) + BN - 1) / BN;
-    b0 = p.window == 0 ? b1 : max(a1, max(0, p_lo + 1 - p.window) / BN);
-  }
-  const int n_all = a1 + max(0, b1 - b0);
-  const int j_lo = (int)((int64_t)n_all * blockIdx.y / p.splits);
-  const int n_it = (int)((int64_t)n_all * (blockIdx.y + 1) / p.splits) - j_lo;
-  // O is taken out after key tile j
-  auto last_of = [&](int j) { return j + 1 == n_it || (PARTS > 1 && (j + 1) % kTaSegment == 0); };
-  auto key_tile = [&](int j) { return (j_lo + j < a1 ? j_lo + j : b0 + j_lo + j - a1) * BN; };
-
   if (tid == 0) {
+    tma_prefetch_map(&p.qmap);
+    tma_prefetch_map(&p.kmap);
+    tma_prefetch_map(&p.vmap);
     for (int s = 0; s < ST; ++s) {
       mbar_init(bar_full(s), 1);
       mbar_init(bar_empty(s), 1);
@@ -205,6 +177,38 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     s_stop = 0;
   }
   if (warp == 10) tmem_alloc<512>(smem_u32(&s_tmem));
+  grid_dep_wait();
+  grid_dep_launch();
+  if (p.q_offsets && tid == 0 && (blockIdx.x | blockIdx.y) == 0 && p.q_offsets[p.B] > p.total_q)
+    record_error(kCheckPosition, p.B, p.q_offsets[p.B], p.total_q);  // rows past those of q are skipped
+  // later rows first, all heads of a tile together: the longest rows start first
+  const int slot_id = (int)((gridDim.x - 1 - blockIdx.x) / p.n_listed), y = (int)(blockIdx.x % p.n_listed);
+  TaPlace at;
+  const bool some = ta_locate(p, slot_id, &at);
+  const int b = at.b, i0 = at.i0, n = at.n, q0 = at.q0, off = at.off, L = at.L;
+  const int g = p.heads[y];
+  const bool dense = p.roles[g] == 1;
+  const int PT = p.PT;
+  // tokens of this CTA (one minimum of a difference: min(min(2 PT, n - i0), total_q - q0 - i0) came out of
+  // nvcc 12.9 without its second term)
+  const int row_end = min(q0 + n, p.total_q), np = min(row_end - (q0 + i0), 2 * PT);
+  const int tiles = !some ? 0 : np > PT ? 2 : 1;
+  // key tiles that some row sees: [0, a1) and [b0, b1)
+  const int p_lo = p.causal ? max(L - n + i0, -1) : L - 1;
+  const int p_hi = p.causal ? max(L - n + i0 + np - 1, -1) : L - 1;
+  int a1 = 0, b0 = 0;
+  const int b1 = (p_hi + BN) / BN;  // ceil((p_hi + 1) / BN)
+  if (!dense) {
+    a1 = (min(p.sink, p_hi + 1) + BN - 1) / BN;
+    b0 = p.window == 0 ? b1 : max(a1, max(0, p_lo + 1 - p.window) / BN);
+  }
+  const int n_all = some ? a1 + max(0, b1 - b0) : 0;
+  const int j_lo = (int)((int64_t)n_all * blockIdx.y / p.splits);
+  const int n_it = (int)((int64_t)n_all * (blockIdx.y + 1) / p.splits) - j_lo;
+  // O is taken out after key tile j
+  auto last_of = [&](int j) { return j + 1 == n_it || (PARTS > 1 && (j + 1) % kTaSegment == 0); };
+  auto key_tile = [&](int j) { return (j_lo + j < a1 ? j_lo + j : b0 + j_lo + j - a1) * BN; };
+
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -215,8 +219,6 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     regs_dec<kTaRegsOther>();
     if (warp == 8 && n_it > 0) {  // ---------------------------------------------- loads
       if (lane == 0) {
-        tma_prefetch_map(&p.kmap);
-        tma_prefetch_map(&p.vmap);
         mbar_expect_tx(bar_q, tiles * (D / 64) * 128 * PT * p.G);
         for (int t = 0; t < tiles; ++t)
           for (int h = 0; h < D / 64; ++h)
@@ -555,7 +557,7 @@ struct MergeParams {
   uint8_t heads[kMaxHeads];
 };
 
-constexpr int kTmThreads = 256, kTmFlight = 4;
+constexpr int kTmThreads = 256, kTmFlight = 8;
 
 // grid (32 (row, q head of the group) pairs, listed heads): a pair per lane, so that the partials of a
 // tile are read as they were written; warps share the D / 4 pieces of the rows.  Partials are added in
@@ -619,16 +621,14 @@ __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParam
     return reinterpret_cast<const float4*>(a);
   };
   const int nt = ns + no + np;
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int s = 0; s < nt; ++s) M = fmaxf(M, ml_of(s).x);
   float4 acc[NC];
-  float l = 0.f;
+  float M = -INFINITY, l = 0.f;
 #pragma unroll
   for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < nt; s0 += kTmFlight) {
     float4 v[kTmFlight][NC];
     float2 ml[kTmFlight];
+    float top = M;
 #pragma unroll
     for (int k = 0; k < kTmFlight; ++k) {
       ml[k] = make_float2(-INFINITY, 0.f);
@@ -636,14 +636,25 @@ __global__ void __launch_bounds__(kTmThreads) tile_merge_kernel(const MergeParam
         ml[k] = ml_of(s0 + k);
         int64_t step;
         const float4* a = acc_of(s0 + k, &step);
-        if (ml[k].x != -INFINITY)  // else nothing was seen, and its acc may never have been written
 #pragma unroll
-          for (int c = 0; c < NC; ++c) v[k][c] = a[(warp * NC + c) * step];
+        for (int c = 0; c < NC; ++c) v[k][c] = a[(warp * NC + c) * step];
       }
     }
 #pragma unroll
+    for (int k = 0; k < kTmFlight; ++k) top = fmaxf(top, ml[k].x);
+    const float al = M == -INFINITY ? 0.f : ex2(M - top);
+    M = top;
+    l *= al;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      acc[c].x *= al;
+      acc[c].y *= al;
+      acc[c].z *= al;
+      acc[c].w *= al;
+    }
+#pragma unroll
     for (int k = 0; k < kTmFlight; ++k) {
-      if (ml[k].x == -INFINITY) continue;
+      if (ml[k].x == -INFINITY) continue;  // nothing was seen, and its acc may never have been written
       const float w = ex2(ml[k].x - M);
       l = fmaf(w, ml[k].y, l);
 #pragma unroll
