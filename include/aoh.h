@@ -500,7 +500,9 @@ aoh_status aoh_kv_append_at(const void* q_new, int32_t n_q_heads, const void* k_
  *              bf16, the result is rounded once.  bf16, unlike the decode calls,
  *              because a prompt's output is the next product's bf16 operand
  *   workspace  device, 256-byte aligned, >= aoh_stream_prefill_workspace_size
- *              bytes (any contents; 0 bytes: may be NULL)
+ *              bytes (any contents; 0 bytes: may be NULL).  Here and in the calls
+ *              below calls that may run at the same time, captured ones among
+ *              them, need workspaces of their own
  * A row that sees nothing (n_b > L_b, or sink = window = 0) gives zeros.
  * K and V of positions [0, L_b) must be finite; slots past L_b may hold anything.
  * n_q_heads / n_kv_heads <= 32; batch <= 65535.
@@ -531,7 +533,8 @@ size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_hea
  *              sum over the P_i prefix tokens and the L_b own tokens of
  *              softmax(scale * q_h . k_t) * v_t; zeros when there is no token
  *   workspace  device, 256-byte aligned, >= aoh_prefix_decode_workspace_size
- *              bytes, zero-filled once before its first use
+ *              bytes (any contents)
+ * Softmax, weights and sums are fp32.  A prefix without sequences is not read.
  * K and V of held positions must be finite; slots past a length may hold anything.
  * Heads that the caches do not store are left as they are.  n_q_heads /
  * n_kv_heads <= 32; batch <= 65535.
@@ -558,7 +561,8 @@ size_t aoh_prefix_decode_workspace_size(const aoh_kv_cache* prefix, const aoh_kv
  *              [0, L_b) are left as they are
  *   out        device fp32 [B][n_q_heads][d], 16-byte aligned
  *   workspace  device, 256-byte aligned, >= aoh_accum_decode_workspace_size
- *              bytes, zero-filled once before its first use
+ *              bytes (any contents)
+ * K and V of positions [0, L_b) must be finite; slots past L_b may hold anything.
  * n_q_heads / n_kv_heads <= 32; batch <= 65535.
  */
 aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, float scale,

@@ -164,3 +164,10 @@ def test_binding_checks_tensors():
                  lambda: B.cache_evict(c, f, 4, 0, 0, c, None, None, None, None, ws)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_refuses_ints_that_would_be_cut():
+    for name in ("sink", "window"):
+        with pytest.raises(ValueError):
+            B._int32("x", **{name: 2 ** 32})
+    B._int32("x", sink=2 ** 31 - 1, window=-2 ** 31)

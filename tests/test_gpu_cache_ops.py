@@ -225,6 +225,60 @@ def test_prefill_in_chunks_equals_the_whole_prompt():
     check_prefill(c, q[400:], [113], roles, 4, 77, 0.1, out, rows=(0, 5, 80))
 
 
+@pytest.mark.parametrize("hkv,G,d", [(2, 4, 128), (1, 7, 64)])
+def test_prefill_few_rows_on_a_long_cache(hkv, G, d):
+    # few rows: the key range is split over CTAs and joined by a second launch
+    new, ctx = [1, 3, 0, 2], [5000, 9000, 40, 0]
+    c = Cache(75, [a + b for a, b in zip(new, ctx)], hkv, d, room=1)
+    q = queries(76, sum(new) + 1, hkv * G, d)
+    for roles, sink, window in (([DENSE] * hkv, 0, 0), ([STREAM] * hkv, 700, 3001)):
+        got = {}
+        got.update(launches_of(lambda: got.setdefault("out", run_prefill(c, q, new, roles, sink, window, 0.11))))
+        assert got["tile_attend_kernel"] == got["tile_merge_kernel"] == 2
+        check_prefill(c, q, new, roles, sink, window, 0.11, got["out"])
+
+
+def grow(c):
+    """Keys that outgrow everything before them, late in every sequence (the reference value has to move)."""
+    for b, n in enumerate(c.lens):
+        for at, f in ((n // 2, 8.0), (n - n // 5, 30.0)):
+            if n > 8:
+                c.kh[c.off[b] + at] = (c.kh[c.off[b] + at].float() * f).bfloat16()
+    c.k.copy_(c.kh)
+
+
+def test_prefill_maxima_that_grow_along_the_row():
+    c = Cache(77, [700], 2, 128)
+    grow(c)
+    q = queries(78, 300, 8, 128)
+    out = run_prefill(c, q, [300], [DENSE, STREAM], 4, 333, 1.5)
+    check_prefill(c, q, [300], [DENSE, STREAM], 4, 333, 1.5, out, rows=(0, 100, 200, 299))
+
+
+def test_prefill_many_sequences():
+    new = [(3 * b) % 4 for b in range(1100)]
+    c = Cache(79, [n + (7 * b) % 5 for b, n in enumerate(new)], 1, 64, room=1)
+    q = queries(80, sum(new), 2, 64)
+    out = run_prefill(c, q, new, [STREAM], 1, 2, 0.2)
+    check_prefill(c, q, new, [STREAM], 1, 2, 0.2, out)
+
+
+def test_prefill_offsets_past_the_rows_are_recorded():
+    c = Cache(83, [20], 1, 64)
+    q = queries(84, 3, 2, 64).cuda()
+    big = torch.full((9, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    kv = c.kv()
+    B.stream_prefill(q, kv, i32([0, 5]), [DENSE], 0, 0, 0.1, big[:3],
+                     B.workspace(B.stream_prefill_workspace_size(kv, 2, 3, [DENSE], 0, 0), "cuda"))
+    st, detail = B.device_check()
+    assert st == 6 and detail[0] == 1
+    assert bool((big[3:] == 7.0).all())
+    for i in range(3):  # the rows that exist stand at L - 5 + i
+        k, v = c.rows(0, 0)
+        ref = attend(q[i, 0].cpu().double(), k, v, torch.arange(20) <= 15 + i, 0.1)[0]
+        assert float((big[i, 0].cpu().double() - ref).abs().max()) <= 2 * 2.0 ** -8 * float(v.abs().max()) + 1e-3
+
+
 # ----------------------------------------------------------------------------------- shared prefix
 
 def run_prefix(p, c, q, start, scale):
@@ -306,6 +360,37 @@ def test_prefix_sequence_outside_every_range_is_recorded():
     check_prefix(p, c, q, None, 0.1, out.cpu())
 
 
+@pytest.mark.parametrize("G,nb", [(8, 5), (7, 40), (1, 129), (32, 2)])
+def test_prefix_long_rows_and_growing_maxima(G, nb):
+    # rows past the 512 tokens that an accumulator gathers, several splits, maxima that grow along them
+    p, c = Cache(115, [5003], 1, 128), Cache(116, [(31 * b) % 150 for b in range(nb)], 1, 128, room=1)
+    q = queries(117, nb, G, 128)
+    out = run_prefix(p, c, q, None, 0.09)
+    check_prefix(p, c, q, None, 0.09, out, seqs=(0, 1, nb // 2, nb - 1))
+    grow(p)
+    grow(c)
+    out = run_prefix(p, c, q, None, 1.1)
+    check_prefix(p, c, q, None, 1.1, out, seqs=(0, 1, nb // 2, nb - 1))
+
+
+def test_prefix_many_sequences():
+    nb = 1100
+    p, c = Cache(118, [130, 5, 700], 1, 64), Cache(119, [(7 * b) % 4 for b in range(nb)], 1, 64, room=1)
+    q = queries(120, nb, 2, 64)
+    start = (0, 3, 600, nb)
+    out = run_prefix(p, c, q, start, 0.13)
+    check_prefix(p, c, q, start, 0.13, out, seqs=(0, 2, 3, 599, 600, 900, nb - 1))
+
+
+@pytest.mark.parametrize("start", [(0, 2, 2, 6), (0, 0, 5, 6), (0, 6, 6, 6)])
+def test_prefix_groups_of_few_rows(start):
+    p = Cache(94, [300, 0, 129], 2, 64, room=1)
+    c = Cache(95, [0, 70, 1, 64, 200, 3], 2, 64)
+    q = queries(96, 6, 10, 64)
+    out = run_prefix(p, c, q, start, 0.12)
+    check_prefix(p, c, q, start, 0.12, out)
+
+
 # ----------------------------------------------------------------------------------- accumulated weights
 
 def check_accum(c, q, scale, decay, mass_in, out, mass_out):
@@ -352,6 +437,36 @@ def test_accum_matches_the_formula(hkv, G, d, lens):
     B.accum_decode(q.cuda(), kv, 0.1, 0.9, mass.cuda(), other, out, ws)
     for b, L in enumerate(lens):
         assert torch.equal(inplace[:, c.off[b]:c.off[b] + L], other[:, c.off[b]:c.off[b] + L])
+
+
+@pytest.mark.parametrize("nb", [300, 1100])
+def test_accum_many_sequences(nb):
+    c = Cache(124, [(13 * b) % 90 if b % 3 else 0 for b in range(nb)], 1, 64, room=1)
+    q = queries(125, nb, 3, 64)
+    mass = torch.rand((1, c.T), generator=torch.Generator().manual_seed(126))
+    kv = c.kv()
+    out, mo = torch.full(q.shape, 7.0, device="cuda"), torch.full((1, c.T), 7.0, device="cuda")
+    B.accum_decode(q.cuda(), kv, 0.2, 0.5, mass.cuda(), mo, out, B.workspace(B.accum_decode_workspace_size(kv, 3), "cuda"))
+    torch.cuda.synchronize()
+    check_device()
+    check_accum(c, q, 0.2, 0.5, mass, out.cpu(), mo.cpu())
+
+
+def test_accum_long_ragged_rows():
+    # rows cut over many CTAs, with ring rounds to spare, and rows that share a CTA
+    c = Cache(127, [20001, 3, 64, 9000, 0, 777, 12345], 2, 128, room=1)
+    grow(c)
+    q = queries(128, 7, 14, 128)
+    kv = c.kv()
+    ws = B.workspace(B.accum_decode_workspace_size(kv, 14), "cuda")
+    out, mo = torch.full(q.shape, 7.0, device="cuda"), torch.full((2, c.T), 7.0, device="cuda")
+    B.accum_decode(q.cuda(), kv, 0.3, 1.0, None, mo, out, ws)
+    again = torch.full_like(mo, 7.0)
+    B.accum_decode(q.cuda(), kv, 0.3, 1.0, None, again, torch.empty_like(out), ws)
+    torch.cuda.synchronize()
+    check_device()
+    assert torch.equal(mo, again)
+    check_accum(c, q, 0.3, 1.0, None, out.cpu(), mo.cpu())
 
 
 def test_accum_layouts_and_slots():
@@ -476,6 +591,79 @@ def test_evict_records_a_region_too_small():
 
 
 # ----------------------------------------------------------------------------------- together
+
+def test_nothing_held_anywhere():
+    c, p = Cache(175, [0, 0], 2, 128, room=4), Cache(176, [0], 2, 128, room=1)
+    d = Cache(177, [0, 0], 2, 128, room=4)
+    q = queries(178, 2, 4, 128).cuda()
+    kv = c.kv()
+    out, mo = torch.full((2, 4, 128), 7.0, device="cuda"), torch.full((2, c.T), 7.0, device="cuda")
+    B.accum_decode(q, kv, 0.1, 1.0, None, mo, out, B.workspace(B.accum_decode_workspace_size(kv, 4), "cuda"))
+    assert bool((out == 0).all()) and bool((mo == 7.0).all())
+    out.fill_(7.0)
+    B.prefix_decode(q, p.kv(), None, kv, 0.1, out, B.workspace(B.prefix_decode_workspace_size(p.kv(), kv, 4), "cuda"))
+    assert bool((out == 0).all())
+    pout = torch.full_like(q, 7.0)
+    B.stream_prefill(q, kv, i32([0, 1, 2]), [DENSE, STREAM], 1, 1, 0.1, pout,
+                     B.workspace(B.stream_prefill_workspace_size(kv, 4, 2, [DENSE, STREAM], 1, 1), "cuda"))
+    assert bool((pout == 0).all())
+    idx, count = torch.zeros((2, 2, 3), dtype=torch.int32, device="cuda"), i32([[7, 7], [7, 7]])
+    lengths = i32([7, 7])
+    B.cache_evict(kv, mo, 3, 1, 1, d.kv(), lengths, None, idx, count, B.workspace(B.cache_evict_workspace_size(kv), "cuda"))
+    assert lengths.tolist() == [0, 0] and bool((count == 0).all()) and bool((idx == -1).all())
+    check_device()
+
+
+def test_append_at_leaves_a_refused_sequence_alone():
+    off = [0, 4, 8, 12]
+    k, v = torch.zeros((12, 1, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((12, 1, 64), dtype=torch.bfloat16, device="cuda")
+    lengths, positions = i32([3, 4, 2]), i32([30, 9, -1])
+    kv = B.make_kv(k, v, i32(off), 4, 12, lengths=lengths)
+    kn, vn = queries(188, 3, 1, 64).cuda(), queries(189, 3, 1, 64).cuda()
+    B.kv_append_at(None, kn, vn, 1e4, kv, None, 0, lengths, positions, None)
+    st, detail = B.device_check()
+    assert st == 6 and detail[0] == 4
+    assert lengths.tolist() == [4, 4, 2] and positions.tolist() == [31, 9, -1]
+    assert torch.equal(v[3], vn[0]) and bool((v[4:] == 0).all()) and bool((k[4:] == 0).all())
+    want = rope64(kn[0, 0].cpu(), 30, 1e4)
+    assert float((k[3, 0].cpu().double() - want).abs().max()) <= 2.0 ** -8 * float(want.abs().max())
+
+
+def test_calls_on_two_streams_at_once():
+    """Steps with workspaces of their own, on two streams at the same time: the results of one after the other."""
+    c = [Cache(210 + i, [4000, 3000, 17], 2, 128) for i in range(2)]
+    q = [queries(212 + i, 3, 8, 128).cuda() for i in range(2)]
+    own = [Cache(214 + i, [20 * b for b in range(12)], 2, 128) for i in range(2)]
+    qp = [queries(216 + i, 12, 8, 128).cuda() for i in range(2)]
+    steps = []
+    for i in range(2):
+        acc = AccumDecodeStep(c[i].k, c[i].v, c[i].offsets, c[i].max_len, c[i].T, 8, 0.1)
+        pre = PrefillStep(c[i].k, c[i].v, c[i].offsets, c[i].max_len, c[i].T, 8, [DENSE, STREAM], 4, 900, 0.1, 3)
+        pfx = PrefixDecodeStep(c[i].k, c[i].v, c[i].offsets[:2], 4000, 4000, own[i].k, own[i].v, own[i].offsets, 240,
+                               own[i].T, 8, 0.1)
+        steps.append((acc, pre, pfx, torch.zeros((2, c[i].T), device="cuda"), torch.zeros_like(q[i]), i32([0, 1, 2, 3])))
+
+    def run(i):
+        acc, pre, pfx, mass, out, qo = steps[i]
+        acc(q[i], None, mass)
+        pre(q[i], qo, out)
+        pfx(qp[i])
+        return [acc.out, mass, out, pfx.out]
+
+    alone = [[x.clone() for x in run(i)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                run(i)
+    torch.cuda.synchronize()
+    check_device()
+    for i in range(2):
+        acc, pre, pfx, mass, out, qo = steps[i]
+        for a, b in zip(alone[i], [acc.out, mass, out, pfx.out]):
+            assert torch.equal(a, b)
+
 
 def test_steps_launch_the_kernels():
     c = Cache(181, [700, 300], 2, 128)

@@ -410,6 +410,13 @@ def _want_ws(fn: str, ws: Optional[torch.Tensor], dev: int) -> tuple:
     return ws.data_ptr(), ws.numel()
 
 
+def _int32(fn: str, **values) -> None:
+    """ctypes takes an int of any size and keeps its low 32 bits."""
+    for name, x in values.items():
+        if not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{fn}: {name} = {x} is outside int32")
+
+
 def kv_append_at(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.Tensor, theta: float, kv: KVCache,
                  idom: Optional[torch.Tensor], n_dom: int, lengths: torch.Tensor, positions: torch.Tensor,
                  q_out: Optional[torch.Tensor], stream=None) -> None:
@@ -443,6 +450,7 @@ def stream_prefill(q: torch.Tensor, kv: KVCache, q_offsets: torch.Tensor, roles,
     r = _host_u8(roles)
     if r is not None and len(r) != kv.n_kv_heads:
         raise ValueError(f"{fn}: {len(r)} roles for {kv.n_kv_heads} KV heads")
+    _int32(fn, sink=sink, window=window)
     _check(fn, lib().aoh_stream_prefill(q_p, shape[1], kv, qo_p, shape[0], r if r is None else ctypes.addressof(r), sink,
                                         window, scale, out_p, ws_p, ws_n, _raw_stream(stream, dev)))
 
@@ -490,6 +498,7 @@ def cache_evict(src: KVCache, mass: torch.Tensor, budget: int, sink: int, recent
                 ws: torch.Tensor, stream=None) -> None:
     """Keep the first, the last and the heaviest rows of every head, moved to another cache (aoh_cache_evict)."""
     fn, dev, n, h = "aoh_cache_evict", _device(src, dst), src.batch, src.n_kv_heads
+    _int32(fn, budget=budget, sink=sink, recent=recent)
     m_p = _want(fn, "mass", mass, torch.float32, (h, src.total_tokens), dev)
     len_p = _want(fn, "dst_lengths", dst_lengths, torch.int32, (n,), dev)
     dm_p = None if dst_mass is None else _want(fn, "dst_mass", dst_mass, torch.float32, (dst.n_kv_heads, dst.total_tokens), dev)
