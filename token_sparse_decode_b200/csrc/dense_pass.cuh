@@ -17,8 +17,11 @@
 // sub-tiles, tokens on the M side of mma.m16n8k16 (the query rows are the N side: 7 rows fill 7 of
 // 8 columns).  Weights enter the product with V as three bf16 terms, so that fp32 outputs keep
 // fp32 weights, and every sub-tile's product starts from zero and is added by the FMA units: the
-// tensor cores' own accumulation rounds towards zero, 3e-6 along 900 tokens.  Bound by the K / V
-// bytes.
+// tensor cores' own accumulation rounds towards zero, 3e-6 along 900 tokens.
+//
+// Bound by the K / V bytes.  Measured (B200): 131072 tokens x 8 heads, d 128 in 90 us, 5.96 TB/s (91 % of
+// the measured copy rate); 48 sequences of 1 to 8000 x 4 heads in 71 us, 5.5 TB/s (a grid of fixed chunks
+// fed by cp.async took 120 and 91 us).
 #pragma once
 
 #include <cuda.h>
