@@ -386,8 +386,12 @@ def kv_append(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torch.T
         int(n_dom), _ptr(lengths), _ptr(q_out), _stream(stream)))
 
 
-def _want(fn: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, dev: int) -> int:
+def _want(fn: str, name: str, t, dtype: torch.dtype, shape: tuple, dev: int) -> int:
     """The address of t, a contiguous tensor of this type and shape on the current device."""
+    if t.__class__ is Owned:
+        if t.dev == dev and t.tensor.shape == shape and t.tensor.dtype is dtype:
+            return t.ptr
+        t = t.tensor
     if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         got = "None" if t is None else f"{t.dtype} {tuple(t.shape)}{'' if t.is_contiguous() else ' (not contiguous)'}"
         raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {got}")
@@ -404,7 +408,19 @@ def _want_q(fn: str, name: str, t: torch.Tensor, rows: Optional[int], d: int, de
     return shape, _want(fn, name, t, torch.bfloat16, shape, dev)
 
 
-def _want_ws(fn: str, ws: Optional[torch.Tensor], dev: int) -> tuple:
+class Owned:
+    """A buffer that a step allocated for its calls: checked once, its address at hand."""
+
+    def __init__(self, t: torch.Tensor):
+        assert t.is_contiguous()
+        self.tensor, self.ptr, self.numel, self.dev = t, t.data_ptr(), t.numel(), t.get_device()
+
+
+def _want_ws(fn: str, ws, dev: int) -> tuple:
+    if ws.__class__ is Owned and ws.dev == dev:
+        return ws.ptr, ws.numel
+    if ws.__class__ is Owned:
+        ws = ws.tensor
     if ws is None or ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.get_device() != dev:
         raise ValueError(f"{fn}: the workspace must be a contiguous uint8 tensor on the current device")
     return ws.data_ptr(), ws.numel()

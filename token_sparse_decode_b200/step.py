@@ -278,12 +278,13 @@ class PrefillStep:
         self.max_total_q = int(max_total_q)
         self.ws = B.workspace(B.stream_prefill_workspace_size(self.kv, n_q_heads, self.max_total_q, self.roles,
                                                               self.sink, self.window), k.device)
+        self._ws = B.Owned(self.ws)
 
     def __call__(self, q: torch.Tensor, q_offsets: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
         if q.shape[0] > self.max_total_q:
             raise ValueError(f"PrefillStep: {q.shape[0]} query rows, built for {self.max_total_q}")
         out = torch.zeros_like(q) if out is None else out
-        B.stream_prefill(q, self.kv, q_offsets, self.roles, self.sink, self.window, self.scale, out, self.ws)
+        B.stream_prefill(q, self.kv, q_offsets, self.roles, self.sink, self.window, self.scale, out, self._ws)
         return out
 
 
@@ -305,11 +306,11 @@ class PrefixDecodeStep:
         self.seq_start, self.scale = seq_start, float(scale)
         self.ws = B.workspace(B.prefix_decode_workspace_size(self.prefix, self.kv, n_q_heads), k.device)
         self.out = torch.zeros((self.kv.batch, n_q_heads, k.shape[2]), dtype=torch.float32, device=k.device)
+        self._ws, self._out = B.Owned(self.ws), B.Owned(self.out)
 
     def __call__(self, q: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        out = self.out if out is None else out
-        B.prefix_decode(q, self.prefix, self.seq_start, self.kv, self.scale, out, self.ws)
-        return out
+        B.prefix_decode(q, self.prefix, self.seq_start, self.kv, self.scale, self._out if out is None else out, self._ws)
+        return self._out.tensor if out is None else out
 
 
 class AccumDecodeStep:
@@ -325,13 +326,13 @@ class AccumDecodeStep:
         self.scale, self.decay = float(scale), float(decay)
         self.ws = B.workspace(B.accum_decode_workspace_size(self.kv, n_q_heads), k.device)
         self.out = torch.zeros((self.kv.batch, n_q_heads, k.shape[2]), dtype=torch.float32, device=k.device)
+        self._ws, self._out = B.Owned(self.ws), B.Owned(self.out)
 
     def __call__(self, q: torch.Tensor, mass_in: Optional[torch.Tensor], mass_out: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        mass_out = mass_in if mass_out is None else mass_out
-        out = self.out if out is None else out
-        B.accum_decode(q, self.kv, self.scale, self.decay, mass_in, mass_out, out, self.ws)
-        return out
+        B.accum_decode(q, self.kv, self.scale, self.decay, mass_in, mass_in if mass_out is None else mass_out,
+                       self._out if out is None else out, self._ws)
+        return self._out.tensor if out is None else out
 
 
 class EvictStep:
@@ -350,10 +351,11 @@ class EvictStep:
         self.idx = torch.empty((self.src.batch, self.src.n_kv_heads, self.budget), dtype=torch.int32, device=k.device)
         self.count = torch.empty((self.src.batch, self.src.n_kv_heads), dtype=torch.int32, device=k.device)
         self.ws = B.workspace(B.cache_evict_workspace_size(self.src), k.device)
+        self._ws, self._idx, self._count = B.Owned(self.ws), B.Owned(self.idx), B.Owned(self.count)
 
     def __call__(self, mass: torch.Tensor, dst_mass: Optional[torch.Tensor], dst_lengths: torch.Tensor):
-        B.cache_evict(self.src, mass, self.budget, self.sink, self.recent, self.dst, dst_lengths, dst_mass, self.idx,
-                      self.count, self.ws)
+        B.cache_evict(self.src, mass, self.budget, self.sink, self.recent, self.dst, dst_lengths, dst_mass, self._idx,
+                      self._count, self._ws)
         return self.idx, self.count
 
 
