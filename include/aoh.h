@@ -512,6 +512,7 @@ aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cac
                               int32_t sink, int32_t window, float scale, void* out,
                               void* workspace, size_t workspace_bytes, void* stream);
 
+/* Enough for every call with at most total_q rows. */
 size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads, int32_t total_q,
                                          const uint8_t* roles, int32_t sink, int32_t window);
 

@@ -171,3 +171,12 @@ def test_binding_refuses_ints_that_would_be_cut():
         with pytest.raises(ValueError):
             B._int32("x", **{name: 2 ** 32})
     B._int32("x", sink=2 ** 31 - 1, window=-2 ** 31)
+
+
+def test_prefill_workspace_is_monotone(lib):
+    r = ctypes.cast(u8(*([1, 2] * 4)), ctypes.c_void_p)
+    c = kv(max_len=100000, total_tokens=200000)
+    sizes = [lib.aoh_stream_prefill_workspace_size(ref(c), 32, n, r, 4, 5000) for n in (1, 2, 50, 300, 1000, 9000, 100000)]
+    assert sizes == sorted(sizes) and sizes[0] > 0
+    assert prefill(lib, c, total=1, n=sizes[0] // 4) == WS
+    assert lib.aoh_stream_prefill_workspace_size(ref(kv(head_dim=96)), 32, 1, r, 4, 5000) == 0

@@ -238,6 +238,25 @@ def test_prefill_few_rows_on_a_long_cache(hkv, G, d):
         check_prefill(c, q, new, roles, sink, window, 0.11, got["out"])
 
 
+def test_prefill_step_serves_fewer_rows_than_it_was_built_for():
+    c = Cache(86, [9000, 300], 2, 128)
+    step = PrefillStep(c.k, c.v, c.offsets, c.max_len, c.T, 8, [DENSE, STREAM], 4, 3000, 0.1, 9300)
+    for new in ([1, 1], [3, 40], [700, 300]):
+        q = queries(87, sum(new), 8, 128)
+        out = step(q.cuda(), i32(offs(new)))
+        torch.cuda.synchronize()
+        check_device()
+        check_prefill(c, q, new, [DENSE, STREAM], 4, 3000, 0.1, out.cpu(), rows=(0, 39, 299))
+
+
+def test_prefill_workspace_covers_every_smaller_call():
+    c = Cache(88, [40000, 9, 9000], 4, 64)
+    kv = c.kv()
+    for roles, sink, window in (([DENSE] * 4, 0, 0), ([STREAM] * 4, 4, 5000), ([SPARSE] * 3 + [STREAM], 1, 2000)):
+        sizes = [B.stream_prefill_workspace_size(kv, 12, n, roles, sink, window) for n in range(1, 4000, 13)]
+        assert sizes == sorted(sizes)
+
+
 def grow(c):
     """Keys that outgrow everything before them, late in every sequence (the reference value has to move)."""
     for b, n in enumerate(c.lens):

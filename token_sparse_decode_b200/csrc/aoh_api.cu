@@ -2141,7 +2141,13 @@ extern "C" {
 size_t aoh_stream_prefill_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads, int32_t total_q,
                                          const uint8_t* roles, int32_t sink, int32_t window) {
   if (check_linear(kv, n_q_heads) != AOH_OK || !roles || check_roles(kv, roles) != AOH_OK || total_q < 1) return 0;
-  return tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, TaTile<128, 1>::BN, false).total;
+  // A call with fewer rows may split its key range where this many rows do not: room for whichever needs
+  // most (split calls have at most one CTA per SM).
+  const TileWs w = tile_ws(kv, n_q_heads, total_q, kv->batch, roles, sink, window, TaTile<128, 1>::BN, false);
+  const TileWs one = tile_ws(kv, n_q_heads, 1, kv->batch, roles, sink, window, TaTile<128, 1>::BN, false);
+  if (one.splits == 1) return w.total;
+  const size_t rows = (size_t)sm_count() * 2 * 128;
+  return std::max(w.total, align256(sizeof(float) * 2 * rows) + align256(sizeof(float) * rows * kv->head_dim));
 }
 
 aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv, const int32_t* q_offsets,
