@@ -50,8 +50,8 @@ constexpr int kTaRegsSoftmax = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 re
 constexpr int kTaRegsOther = 88;
 constexpr int kTaRegsLaunch = 168;
 constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
-constexpr int kTaSegment = 8;         // key tiles that O gathers (PARTS > 1; 16: 150 us instead of 160 for 96
-                                      // sequences behind two documents, and half as exact again)
+constexpr int kTaSegment = 8;         // key tiles that O gathers (PARTS > 1; 16 instead: 6 % faster on 96
+                                      // sequences behind two documents, and nearly twice as far off)
 constexpr int kTaSplitTiles = 16;     // key tiles of a split at least, where every split leaves partials
 constexpr float kTaGrowth = 60.f;     // log2 of the largest weight before a rescale
 
