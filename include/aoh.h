@@ -585,7 +585,8 @@ size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads
  *   dst        linear cache, same batch / n_kv_heads / head_dim, storing the same
  *              heads, in memory apart from src (overlapping address ranges are
  *              refused).  Its lengths field and k_dom are not used
- *   dst_lengths  device int32 [B], written: n (usually dst's lengths array)
+ *   dst_lengths  device int32 [B], written: n (usually dst's lengths array; src's is
+ *              allowed too: one array that follows the rows from buffer to buffer)
  *   dst_mass   device fp32 [Hkv][dst->total_tokens] or NULL: the kept rows' mass,
  *              zeros in the rest of the sequence's region
  *   idx, count device int32 [B][Hkv][budget] and [B][Hkv]: the kept positions,

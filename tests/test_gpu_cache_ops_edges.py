@@ -1,0 +1,34 @@
+"""The cache operators where their arguments share memory, their numbers are extreme or their
+workspaces are used again: each against the definition, in float64 or exactly."""
+
+import pytest
+import torch
+
+from gpu_helpers import check_device
+from test_gpu_cache_ops import Cache, check_evict, draw_mass, i32
+from token_sparse_decode_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+# ----------------------------------------------------------------------------------- eviction
+
+def test_evict_with_one_lengths_array_for_both_caches():
+    # far more copy blocks than run at once: those that start late must keep what the first ones keep
+    c = Cache(301, [2500 + 11 * b for b in range(64)], 4, 64)
+    budget, sink, recent = 1000, 4, 100
+    mass = draw_mass(302, 4, c.T, "plain")
+    dst = Cache(303, [0] * 64, 4, 64, room=budget)
+    dst.max_len = budget
+    lengths = i32(c.lens)  # the source's, and written as the destination's
+    src = B.make_kv(c.k, c.v, c.offsets, c.max_len, c.T, lengths=lengths)
+    dst.k.fill_(5.0)
+    dst.v.fill_(6.0)
+    res = dict(dst=dst, idx=torch.full((64, 4, budget), -7, dtype=torch.int32, device="cuda"),
+               count=torch.full((64, 4), -7, dtype=torch.int32, device="cuda"),
+               mass=torch.full((4, dst.T), 7.0, device="cuda"), lengths=lengths)
+    ws = B.workspace(B.cache_evict_workspace_size(src), "cuda")
+    B.cache_evict(src, mass.cuda(), budget, sink, recent, dst.kv(), lengths, res["mass"], res["idx"], res["count"], ws)
+    torch.cuda.synchronize()
+    check_device()
+    check_evict(c, mass, budget, sink, recent, res)

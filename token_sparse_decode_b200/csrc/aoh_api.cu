@@ -2315,6 +2315,7 @@ aoh_status aoh_cache_evict(const aoh_kv_cache* src, const float* mass, int32_t b
   bind_cache(ep, src);
   for (int g = 0; g < dst->n_kv_heads; ++g) ep.dslot[g] = slot_of(dst, g);
   ep.idx = idx;
+  ep.count = count;
   ep.k = static_cast<const uint16_t*>(src->k);
   ep.v = static_cast<const uint16_t*>(src->v);
   ep.stride_tok = src->stride_tok;

@@ -27,6 +27,7 @@ struct EvictParams {
   const int32_t* offsets;     // [B + 1]
   const int32_t* lengths;     // [B] or null
   const int32_t* idx;         // [B][Hkv][budget]
+  const int32_t* count;       // [B][Hkv]
   // source rows
   const uint16_t* k;
   const uint16_t* v;
@@ -69,7 +70,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_key_kernel(const EvictPar
 }
 
 // grid (chunks of kEvictRows kept rows, listed heads, sequences): D / 8 lanes copy one row's 16-byte
-// pieces of K and V; a thread has the loads of all its rows in flight before the first store.
+// pieces of K and V; a thread has the loads of all its rows in flight before the first store.  The rows
+// kept are taken from the select's counts, not from the source's lengths: dlengths may be that array.
 constexpr int kEvictRows = 64;
 
 template <int D>
@@ -80,9 +82,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictPa
   constexpr int RPP = kEvictThreads / LPR;     // rows per pass
   constexpr int NP = kEvictRows / RPP;         // passes
   const int b = blockIdx.z, g = p.heads[blockIdx.y], tid = threadIdx.x;
-  int off;
-  const int L = seq_length(p.offsets, p.lengths, b, false, &off);
-  const int n = min(L, p.budget);
+  const int off = p.offsets[b], cap = p.offsets[b + 1] - off;
+  const int n = p.count[(int64_t)b * p.Hkv + g];
   const int doff = p.doffsets[b], dcap = p.doffsets[b + 1] - doff;
   const bool fits = n <= dcap && doff >= 0 && (int64_t)doff + dcap <= p.dT;
   if (!fits && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) record_error(kCheckCapacity, b, n, dcap);
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictPa
   for (int i = 0; i < NP; ++i) {
     const int j = j0 + i * RPP + r0;
     pos[i] = j < n ? lst[j] : -1;
-    if (j < n && (pos[i] < 0 || pos[i] >= L)) {
+    if (j < n && (pos[i] < 0 || pos[i] >= cap)) {
       record_error(kCheckPosition, b, g, pos[i]);
       pos[i] = -1;
     }
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictPa
     }
   if (p.dmass && tid < kEvictRows && j0 + tid < n) {
     const int s = lst[j0 + tid];
-    if (s >= 0 && s < L) p.dmass[(int64_t)g * p.dT + doff + j0 + tid] = p.mass[(int64_t)g * p.T + off + s];
+    if (s >= 0 && s < cap) p.dmass[(int64_t)g * p.dT + doff + j0 + tid] = p.mass[(int64_t)g * p.T + off + s];
   }
 }
 
