@@ -591,8 +591,8 @@ size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads
  *              zeros in the rest of the sequence's region
  *   idx, count device int32 [B][Hkv][budget] and [B][Hkv]: the kept positions,
  *              ascending, -1 padded, and n (layouts of aoh_topk_select)
- *   workspace  device, 256-byte aligned, >= aoh_cache_evict_workspace_size bytes,
- *              zero-filled once before its first use
+ *   workspace  device, 256-byte aligned, >= aoh_cache_evict_workspace_size bytes (any
+ *              contents)
  * A sequence whose kept rows do not fit its region in dst is not copied and gets
  * length 0 (device check 4).  batch <= 65535.  Rows up to 4 M positions.
  */

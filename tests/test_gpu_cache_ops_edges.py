@@ -4,7 +4,7 @@ workspaces are used again: each against the definition, in float64 or exactly.""
 import pytest
 import torch
 
-from gpu_helpers import check_device
+from gpu_helpers import check_device, launches_of
 from test_gpu_cache_ops import Cache, check_evict, draw_mass, i32
 from token_sparse_decode_b200 import binding as B
 
@@ -32,3 +32,26 @@ def test_evict_with_one_lengths_array_for_both_caches():
     torch.cuda.synchronize()
     check_device()
     check_evict(c, mass, budget, sink, recent, res)
+
+
+def test_evict_of_very_long_rows_on_a_workspace_that_served_another_cache():
+    # more than 262144 positions: scores and histograms in the workspace, at places that depend on the cache
+    kinds, ws = ("special", "ties", "plain"), None
+    for i, (lens, hkv) in enumerate((([300_000], 2), ([270_000, 9], 1), ([290_000], 1))):
+        c = Cache(311 + i, lens, hkv, 64)
+        mass, dst = draw_mass(315 + i, hkv, c.T, kinds[i]), Cache(318, [0] * len(lens), hkv, 64, room=4000)
+        dst.max_len = 4000
+        dst.k.fill_(5.0)
+        dst.v.fill_(6.0)
+        need = B.cache_evict_workspace_size(c.kv())
+        if ws is None:
+            ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+        assert need <= ws.numel()
+        res = dict(dst=dst, idx=torch.full((len(lens), hkv, 4000), -7, dtype=torch.int32, device="cuda"),
+                   count=torch.full((len(lens), hkv), -7, dtype=torch.int32, device="cuda"),
+                   mass=torch.full((hkv, dst.T), 7.0, device="cuda"), lengths=i32([-7] * len(lens)))
+        got = launches_of(lambda: B.cache_evict(c.kv(), mass.cuda(), 4000, 4, 500, dst.kv(), res["lengths"], res["mass"],
+                                                res["idx"], res["count"], ws))
+        check_device()
+        assert got["evict_key_kernel"] == got["select_hist_kernel"] == got["select_write_kernel"] == 1
+        check_evict(c, mass, 4000, 4, 500, res)

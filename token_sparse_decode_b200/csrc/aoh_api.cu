@@ -2365,6 +2365,9 @@ aoh_status aoh_cache_evict(const aoh_kv_cache* src, const float* mass, int32_t b
       return s;
   } else {
     const int chunks = (int)std::max<int64_t>(1, ceil_div(src->max_len, kEvictThreads * 4));
+    const SelectWs sw = select_ws(src);  // histograms and candidate counts, one behind the other
+    ep.counters = reinterpret_cast<uint32_t*>(ws + off_select + sw.hist);
+    ep.n_counters = (int64_t)((sw.cand - sw.hist) / sizeof(uint32_t));
     if ((s = launch_dependent(evict_key_kernel, dim3(chunks, ep.n_listed, ep.B), kEvictThreads, 0, 0, st, ep)) != AOH_OK ||
         (s = count_launch(AOH_KERNEL_EVICT_KEY, st)) != AOH_OK)
       return s;

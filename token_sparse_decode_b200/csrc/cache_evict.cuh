@@ -24,6 +24,8 @@ namespace aoh {
 struct EvictParams {
   const float* mass;          // [Hkv][T]
   float* scores;              // [Hkv][T]
+  uint32_t* counters;         // [n_counters] the select's counters in the workspace
+  int64_t n_counters;
   const int32_t* offsets;     // [B + 1]
   const int32_t* lengths;     // [B] or null
   const int32_t* idx;         // [B][Hkv][budget]
@@ -50,10 +52,15 @@ struct EvictParams {
 
 constexpr int kEvictThreads = 256;
 
-// grid (position chunks of kEvictThreads * 4, listed heads, sequences)
+// grid (position chunks of kEvictThreads * 4, listed heads, sequences).  Also clears the counters that the
+// select behind it expects at zero: their place depends on the cache, and the workspace may have
+// served another one.
 __global__ void __launch_bounds__(kEvictThreads) evict_key_kernel(const EvictParams p) {
   grid_dep_wait();
   grid_dep_launch();
+  const int64_t block = ((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x;
+  const int64_t threads = (int64_t)gridDim.x * gridDim.y * gridDim.z * kEvictThreads;
+  for (int64_t i = block * kEvictThreads + threadIdx.x; i < p.n_counters; i += threads) p.counters[i] = 0u;
   const int b = blockIdx.z, g = p.heads[blockIdx.y];
   int off;
   const int L = seq_length(p.offsets, p.lengths, b, false, &off);
