@@ -576,7 +576,7 @@ size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads
  * aoh_cache_evict -- keep the tokens that attention has used.  Of the L_b
  * positions of every (sequence, KV head) the call keeps n = min(budget, L_b): the
  * first `sink`, the last `recent`, and of the others those with the largest
- * mass (equal: the lower position; a NaN counts as the smallest).  Each head
+ * mass (equal: the lower position; a NaN counts as -inf).  Each head
  * keeps positions of its own.  The kept rows are written, in position order, to
  * slots 0 .. n - 1 of the sequence's region in another cache, from which any
  * decode call goes on (keys keep the rotation of their original positions).

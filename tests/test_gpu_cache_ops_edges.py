@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_helpers import check_device, launches_of
-from test_gpu_cache_ops import Cache, check_evict, draw_mass, i32
+from test_gpu_cache_ops import Cache, check_evict, draw_mass, i32, run_evict
 from token_sparse_decode_b200 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +55,15 @@ def test_evict_of_very_long_rows_on_a_workspace_that_served_another_cache():
         check_device()
         assert got["evict_key_kernel"] == got["select_hist_kernel"] == got["select_write_kernel"] == 1
         check_evict(c, mass, 4000, 4, 500, res)
+
+
+@pytest.mark.parametrize("L", [200, 140_000, 270_000])  # the cluster select, and the two selects of longer rows
+def test_evict_takes_an_infinite_weight_before_the_largest_finite_one(L):
+    c = Cache(321, [L], 1, 64)
+    mass = torch.full((1, L), torch.finfo(torch.float32).max)
+    mass[0, 100:110] = float("inf")
+    mass[0, 150:160] = -float("inf")
+    for budget, sink, recent in ((13, 2, 1), (13, 0, 0), (12, 6, 6)):
+        res = run_evict(c, mass, budget, sink, recent, budget)
+        check_device()
+        check_evict(c, mass, budget, sink, recent, res)

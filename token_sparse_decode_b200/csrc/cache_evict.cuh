@@ -8,7 +8,7 @@
 // and lengths'[b] = n.  Each KV head keeps positions of its own, all heads equally many.
 //
 //   select_cluster_kernel<true>  (rows up to 131072 positions) the exact top-n select on the weights,
-//                      keys in registers: protected positions count as +inf, a NaN as the lightest;
+//                      keys in registers: protected positions before every weight, a NaN as the lightest;
 //   evict_key_kernel and the library's select (longer rows): the same with the keys in memory;
 //   evict_copy_kernel  moves the rows.
 // Measured: 32 sequences of 700 to 4500 x 8 heads to 2048 rows in 98 us, the copy 79 us of it (6.7 TB/s

@@ -23,7 +23,6 @@
 #pragma once
 
 #include <cooperative_groups.h>
-#include <float.h>
 
 #include "device_common.cuh"
 
@@ -48,10 +47,10 @@ struct ClusterSelectParams {
 };
 
 // EVICT: the scores are accumulated attention weights; the first `sink` and the last `recent` positions come
-// before all others (+inf), and the others' weights are limited to the finite range (a NaN is the lightest).
+// before all others, and a NaN counts as -inf.  Protected positions get the bits above those of +inf, which no
+// weight has by then, so that +inf stays a weight heavier than any finite one.
 __device__ __forceinline__ float evict_score(float m, int pos, int L, int sink, int recent) {
-  const float lim = m != m ? -INFINITY : fminf(m, FLT_MAX);
-  return (pos < sink || pos >= L - recent) ? INFINITY : lim;
+  return (pos < sink || pos >= L - recent) ? __uint_as_float(0x7fffffffu) : m != m ? -INFINITY : m;
 }
 
 template <bool EVICT>
