@@ -594,7 +594,7 @@ size_t aoh_accum_decode_workspace_size(const aoh_kv_cache* kv, int32_t n_q_heads
  *   workspace  device, 256-byte aligned, >= aoh_cache_evict_workspace_size bytes (any
  *              contents)
  * A sequence whose kept rows do not fit its region in dst is not copied and gets
- * length 0 (device check 4).  batch <= 65535.  Rows up to 4 M positions.
+ * length 0 (device check 4), its dst_mass zeros.  batch <= 65535.  Rows up to 4 M positions.
  */
 aoh_status aoh_cache_evict(const aoh_kv_cache* src, const float* mass, int32_t budget, int32_t sink,
                            int32_t recent, const aoh_kv_cache* dst, int32_t* dst_lengths,

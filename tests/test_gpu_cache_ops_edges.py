@@ -67,3 +67,18 @@ def test_evict_takes_an_infinite_weight_before_the_largest_finite_one(L):
         res = run_evict(c, mass, budget, sink, recent, budget)
         check_device()
         check_evict(c, mass, budget, sink, recent, res)
+
+
+def test_evict_clears_the_weights_of_a_region_too_small():
+    # what is appended to the empty sequence later must not add to weights of tokens that are gone
+    c = Cache(331, [10, 100, 20], 2, 64)
+    mass = draw_mass(332, 2, c.T, "plain")
+    res = run_evict(c, mass, 50, 1, 1, 30)
+    st, detail = B.device_check()
+    assert st == 6 and detail == [4, 1, 50, 30] and res["lengths"].tolist() == [10, 0, 20]
+    off = res["dst"].off
+    assert bool((res["mass"][:, off[1]:off[2]] == 0).all())
+    for b in (0, 2):
+        n = c.lens[b]
+        assert torch.equal(res["mass"][:, off[b]:off[b] + n].cpu(), mass[:, c.off[b]:c.off[b] + n])
+        assert bool((res["mass"][:, off[b] + n:off[b + 1]] == 0).all())

@@ -90,12 +90,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictPa
   constexpr int NP = kEvictRows / RPP;         // passes
   const int b = blockIdx.z, g = p.heads[blockIdx.y], tid = threadIdx.x;
   const int off = p.offsets[b], cap = p.offsets[b + 1] - off;
-  const int n = p.count[(int64_t)b * p.Hkv + g];
+  const int kept = p.count[(int64_t)b * p.Hkv + g];
   const int doff = p.doffsets[b], dcap = p.doffsets[b + 1] - doff;
-  const bool fits = n <= dcap && doff >= 0 && (int64_t)doff + dcap <= p.dT;
-  if (!fits && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) record_error(kCheckCapacity, b, n, dcap);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) p.dlengths[b] = fits ? n : 0;
-  if (!fits) return;
+  const bool region = dcap >= 0 && doff >= 0 && (int64_t)doff + dcap <= p.dT;
+  const int n = region && kept <= dcap ? kept : 0;  // rows moved: all or none
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    if (n < kept || !region) record_error(kCheckCapacity, b, kept, dcap);
+    p.dlengths[b] = n;
+  }
+  if (!region) return;
   const int j0 = blockIdx.x * kEvictRows;
   if (p.dmass) {  // slots past the kept rows start without weight
     float* dm = p.dmass + (int64_t)g * p.dT + doff;
