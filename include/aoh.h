@@ -505,6 +505,7 @@ aoh_status aoh_kv_append_at(const void* q_new, int32_t n_q_heads, const void* k_
  *              them, need workspaces of their own
  * A row that sees nothing (n_b > L_b, or sink = window = 0) gives zeros.
  * K and V of positions [0, L_b) must be finite; slots past L_b may hold anything.
+ * k and v may be NULL, here and in the calls below, where total_tokens is 0.
  * n_q_heads / n_kv_heads <= 32; batch <= 65535.
  */
 aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cache* kv,

@@ -1,0 +1,21 @@
+"""More host-side checks of the cache operators (no device needed)."""
+
+from test_cache_ops_refusals import INVALID, WS, accum, evict, kv, lib, other, prefill, prefix  # noqa: F401 (lib: fixture)
+
+
+def empty(**kw):
+    return kv(**{"k": None, "v": None, "total_tokens": 0, "max_len": 0, **kw})
+
+
+def test_a_cache_without_rows_needs_no_address(lib):
+    # the arguments pass: the missing workspace is what is refused
+    assert accum(lib, empty(), mo=None, ws=None) == WS
+    assert prefix(lib, kv(), empty(), ws=None) == WS and prefix(lib, empty(), kv(), ws=None) == WS
+    assert evict(lib, empty(), other(), mass=None, ws=None) == WS and evict(lib, kv(), empty(), ws=None) == WS
+    assert lib.aoh_accum_decode_workspace_size(empty(), 32) > 0
+    # with rows it does
+    for gone in ("k", "v"):
+        bad = kv(**{gone: None})
+        assert accum(lib, bad) == INVALID and prefill(lib, bad) == INVALID
+        assert prefix(lib, bad, kv()) == INVALID and prefix(lib, kv(), bad) == INVALID
+        assert evict(lib, bad, other()) == INVALID and evict(lib, kv(), other(**{gone: None})) == INVALID

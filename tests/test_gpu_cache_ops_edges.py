@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_helpers import check_device, launches_of
-from test_gpu_cache_ops import Cache, check_evict, draw_mass, i32, run_evict
+from test_gpu_cache_ops import (DENSE, STREAM, Cache, check_evict, check_prefix, draw_mass, i32, queries, run_evict)
 from token_sparse_decode_b200 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,53 @@ def test_evict_clears_the_weights_of_a_region_too_small():
         n = c.lens[b]
         assert torch.equal(res["mass"][:, off[b]:off[b] + n].cpu(), mass[:, c.off[b]:c.off[b] + n])
         assert bool((res["mass"][:, off[b] + n:off[b + 1]] == 0).all())
+
+
+# ----------------------------------------------------------------------------------- caches without rows
+
+def no_rows(batch, hkv, d):
+    """A cache whose tensors have no elements (and so no address)."""
+    k = torch.empty((0, hkv, d), dtype=torch.bfloat16, device="cuda")
+    return B.make_kv(k, torch.empty_like(k), i32([0] * (batch + 1)), 0, 0)
+
+
+@pytest.mark.parametrize("nb", [3, 70])  # the dense pass alone, and tiles
+def test_prefix_decode_when_one_side_has_no_rows(nb):
+    full, zero = Cache(341, [700], 2, 128), Cache(342, [0] * nb, 2, 128)
+    q = queries(343, nb, 8, 128)
+    out = torch.full(q.shape, 7.0, device="cuda")
+    own, prefix = no_rows(nb, 2, 128), no_rows(1, 2, 128)
+    B.prefix_decode(q.cuda(), full.kv(), None, own, 0.1, out,
+                    B.workspace(B.prefix_decode_workspace_size(full.kv(), own, 8), "cuda"))
+    check_device()
+    check_prefix(full, zero, q, None, 0.1, out.cpu(), seqs=(0, 1, nb - 1))
+    c, nothing = Cache(344, [b % 5 for b in range(nb)], 2, 128), Cache(345, [0], 2, 128)
+    B.prefix_decode(q.cuda(), prefix, None, c.kv(), 0.1, out,
+                    B.workspace(B.prefix_decode_workspace_size(prefix, c.kv(), 8), "cuda"))
+    check_device()
+    check_prefix(nothing, c, q, None, 0.1, out.cpu(), seqs=(0, 1, nb - 1))
+    out.fill_(7.0)
+    B.prefix_decode(q.cuda(), prefix, None, own, 0.1, out, B.workspace(B.prefix_decode_workspace_size(prefix, own, 8), "cuda"))
+    check_device()
+    assert bool((out == 0).all())
+
+
+def test_the_other_calls_on_a_cache_without_rows():
+    kv, q = no_rows(3, 2, 64), queries(351, 3, 4, 64).cuda()
+    out, mass = torch.full((3, 4, 64), 7.0, device="cuda"), torch.zeros((2, 0), device="cuda")
+    B.accum_decode(q, kv, 0.1, 0.9, mass, mass, out, B.workspace(B.accum_decode_workspace_size(kv, 4), "cuda"))
+    assert bool((out == 0).all())
+    pout = torch.full_like(q, 7.0)
+    B.stream_prefill(q, kv, i32([0, 1, 1, 3]), [DENSE, STREAM], 1, 1, 0.1, pout,
+                     B.workspace(B.stream_prefill_workspace_size(kv, 4, 3, [DENSE, STREAM], 1, 1), "cuda"))
+    assert bool((pout == 0).all())
+    idx, count = torch.zeros((3, 2, 5), dtype=torch.int32, device="cuda"), torch.full((3, 2), 7, dtype=torch.int32, device="cuda")
+    lengths, ws = i32([7, 7, 7]), B.workspace(B.cache_evict_workspace_size(kv), "cuda")
+    B.cache_evict(kv, mass, 5, 1, 1, no_rows(3, 2, 64), lengths, mass.clone(), idx, count, ws)
+    assert lengths.tolist() == [0, 0, 0] and bool((count == 0).all()) and bool((idx == -1).all())
+    check_device()
+    src = Cache(352, [4, 0, 9], 2, 64)  # rows to keep, and no room
+    B.cache_evict(src.kv(), torch.rand((2, src.T), device="cuda"), 5, 1, 1, no_rows(3, 2, 64), lengths, None, idx, count,
+                  B.workspace(B.cache_evict_workspace_size(src.kv()), "cuda"))
+    st, detail = B.device_check()
+    assert st == 6 and detail[0] == 4 and lengths.tolist() == [0, 0, 0]

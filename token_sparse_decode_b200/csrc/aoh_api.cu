@@ -36,14 +36,16 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
-aoh_status check_kv(const aoh_kv_cache* kv) {
+// `empty_ok`: k and v of a cache without rows may be null (a tensor of no elements has no address)
+aoh_status check_kv(const aoh_kv_cache* kv, bool empty_ok = false) {
   if (!kv) return AOH_ERR_INVALID_ARG;
   if (kv->batch < 0 || kv->n_kv_heads < 1 || kv->n_kv_heads > kMaxHeads) return AOH_ERR_INVALID_ARG;
   if (kv->head_dim != 64 && kv->head_dim != 128) return AOH_ERR_UNSUPPORTED;
   if (kv->max_len < 0 || kv->total_tokens < 0 || kv->total_tokens >= (int64_t(1) << 31))
     return AOH_ERR_INVALID_ARG;
   if (kv->batch == 0) return AOH_OK;
-  if (!kv->k || !kv->v || !kv->offsets) return AOH_ERR_INVALID_ARG;
+  if (!kv->offsets) return AOH_ERR_INVALID_ARG;
+  if ((!kv->k || !kv->v) && !(empty_ok && kv->total_tokens == 0)) return AOH_ERR_INVALID_ARG;
   if (kv->stride_tok < 1 || kv->stride_head < 1) return AOH_ERR_INVALID_ARG;
   if (!aligned16(kv->k) || !aligned16(kv->v) || (kv->stride_tok % 8) || (kv->stride_head % 8))
     return AOH_ERR_ALIGNMENT;
@@ -1795,7 +1797,7 @@ constexpr int kMaxGridZ = 65535;  // sequences of a call whose grids have one la
 
 // checks shared by the calls on a linear cache: descriptor, layout, query heads, batch
 aoh_status check_linear(const aoh_kv_cache* kv, int32_t n_q_heads) {
-  aoh_status s = check_kv(kv);
+  aoh_status s = check_kv(kv, true);
   if (s != AOH_OK) return s;
   if (is_ring(kv)) return AOH_ERR_INVALID_ARG;
   if ((s = check_heads(kv, n_q_heads)) != AOH_OK) return s;
@@ -1856,13 +1858,15 @@ aoh_status encode_map(CUtensorMap* map, const void* base, uint64_t n1, uint64_t 
              : AOH_ERR_UNSUPPORTED;
 }
 
-aoh_status encode_cache(CUtensorMap* k, CUtensorMap* v, const aoh_kv_cache* kv, int tokens) {
+// `spare`: any aligned device address, for the maps of a cache without rows (no tile of it is ever loaded)
+aoh_status encode_cache(CUtensorMap* k, CUtensorMap* v, const aoh_kv_cache* kv, int tokens, const void* spare) {
   int slots = 1;
   for (int g = 0; g < kv->n_kv_heads; ++g)
     if (slot_of(kv, g) != kNoSlot) slots = std::max(slots, slot_of(kv, g) + 1);
   const uint64_t T = (uint64_t)std::max<int64_t>(1, kv->total_tokens);
-  aoh_status s = encode_map(k, kv->k, slots, T, kv->stride_head, kv->stride_tok, kv->head_dim, 1, tokens);
-  return s != AOH_OK ? s : encode_map(v, kv->v, slots, T, kv->stride_head, kv->stride_tok, kv->head_dim, 1, tokens);
+  const void *kb = kv->total_tokens > 0 ? kv->k : spare, *vb = kv->total_tokens > 0 ? kv->v : spare;
+  aoh_status s = encode_map(k, kb, slots, T, kv->stride_head, kv->stride_tok, kv->head_dim, 1, tokens);
+  return s != AOH_OK ? s : encode_map(v, vb, slots, T, kv->stride_head, kv->stride_tok, kv->head_dim, 1, tokens);
 }
 
 // ---- one pass over a whole cache (accumulated weights; the own tokens behind a shared prefix)
@@ -1908,8 +1912,8 @@ aoh_status launch_dense(const void* q, int32_t Hq, const aoh_kv_cache* kv, float
                         float* logits, int logit_pitch, bool late_wait, const DenseWs& w, uint8_t* ws, DenseRows* rows,
                         cudaStream_t st, const aoh_kv_cache* prefix = nullptr, const int32_t* seq_start = nullptr) {
   DenseParams dp{};
-  aoh_status s = encode_cache(&dp.kmap[0], &dp.vmap[0], kv, kDpTile);
-  if (s != AOH_OK || (prefix && (s = encode_cache(&dp.kmap[1], &dp.vmap[1], prefix, kDpTile)) != AOH_OK)) return s;
+  aoh_status s = encode_cache(&dp.kmap[0], &dp.vmap[0], kv, kDpTile, q);
+  if (s != AOH_OK || (prefix && (s = encode_cache(&dp.kmap[1], &dp.vmap[1], prefix, kDpTile, q)) != AOH_OK)) return s;
   if (prefix) {
     dp.pre_offsets = prefix->offsets;
     dp.pre_lengths = prefix->lengths;
@@ -2011,7 +2015,7 @@ aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_ca
                       int64_t total_q, float scale, const TileWs& w, void* workspace, int bn) {
   const int d = kv->head_dim, G = Hq / kv->n_kv_heads, PT = 128 / G;
   aoh_status s = encode_map(&tp.qmap, q, Hq, total_q, d, uint64_t(Hq) * d, d, G, PT);
-  if (s != AOH_OK || (s = encode_cache(&tp.kmap, &tp.vmap, kv, bn)) != AOH_OK) return s;
+  if (s != AOH_OK || (s = encode_cache(&tp.kmap, &tp.vmap, kv, bn, q)) != AOH_OK) return s;
   tp.offsets = kv->offsets;
   bind_cache(tp, kv);
   tp.q_offsets = q_offsets;
