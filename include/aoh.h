@@ -505,6 +505,8 @@ aoh_status aoh_kv_append_at(const void* q_new, int32_t n_q_heads, const void* k_
  *              them, need workspaces of their own
  * A row that sees nothing (n_b > L_b, or sink = window = 0) gives zeros.
  * K and V of positions [0, L_b) must be finite; slots past L_b may hold anything.
+ * Here and in the calls below sums over tokens are fp32 and divided by the sum of the
+ * weights at the end: every scale * q_h . k_t and 2^9 * L_b * max |v| must be finite in fp32.
  * k and v may be NULL, here and in the calls below, where total_tokens is 0.
  * n_q_heads / n_kv_heads <= 32; batch <= 65535.
  */

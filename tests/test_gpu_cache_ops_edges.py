@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from gpu_helpers import check_device, launches_of
-from test_gpu_cache_ops import (DENSE, STREAM, Cache, check_evict, check_prefix, draw_mass, i32, queries, run_evict)
+from test_gpu_cache_ops import (DENSE, STREAM, Cache, check_evict, check_prefill, check_prefix, draw_mass, i32, queries,
+                                run_evict, run_prefill, run_prefix)
 from token_sparse_decode_b200 import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -132,3 +133,38 @@ def test_the_other_calls_on_a_cache_without_rows():
                   B.workspace(B.cache_evict_workspace_size(src.kv()), "cuda"))
     st, detail = B.device_check()
     assert st == 6 and detail[0] == 4 and lengths.tolist() == [0, 0, 0]
+
+
+# ----------------------------------------------------------------------------------- large values
+
+def heavy_late(c, u, gain, values):
+    """Two tokens of every sequence, in its middle and near its end, whose logits with the query u stand `gain` and
+    1.5 gain above the others'; values scaled by `values`."""
+    for b, n in enumerate(c.lens):
+        o = c.off[b]
+        c.kh[o:o + n] = (c.kh[o:o + n].float() * 0.05).bfloat16()
+        for at, f in ((n // 2, 1.0), (n - 1 - n // 9, 1.5)):
+            c.kh[o + at] = (u * (f * gain / float(u @ u))).bfloat16()
+    c.vh.mul_(values)
+    c.k.copy_(c.kh)
+    c.v.copy_(c.vh)
+
+
+@pytest.mark.parametrize("gain", [3.0, 20.0, 27.0])  # 4, 29 and 39 (then 58) powers of two above a row's first tokens
+def test_values_near_the_largest_when_maxima_grow(gain):
+    u = torch.randn(64, generator=torch.Generator().manual_seed(361))
+    big = 2.0 ** 100
+    c = Cache(362, [900, 300], 2, 64)
+    heavy_late(c, u, gain, big)
+    new = [260, 300]
+    q = (u + 0.02 * queries(363, sum(new), 4, 64).float()).bfloat16()
+    out = run_prefill(c, q, new, [DENSE, STREAM], 4, 200, 1.0)
+    assert bool(out[:, :2].isfinite().all())
+    check_prefill(c, q, new, [DENSE, STREAM], 4, 200, 1.0, out, rows=(0, 100, 150, 259, 290))
+    p, own = Cache(364, [1500], 2, 64), Cache(365, [(5 * b) % 40 for b in range(70)], 2, 64)
+    heavy_late(p, u, gain, big)
+    own.vh.mul_(big)
+    own.v.copy_(own.vh)
+    q = (u + 0.02 * queries(366, 70, 4, 64).float()).bfloat16()
+    out = run_prefix(p, own, q, None, 1.0)  # tiles and the dense pass
+    check_prefix(p, own, q, None, 1.0, out, seqs=(0, 1, 7, 69))

@@ -20,9 +20,10 @@
 //     TMEM columns: S_0 / P_0 [0, 128), S_1 / P_1 [128, 256), O_0 [256, 256 + D), O_1 behind it.
 //
 // Softmax.  m is a reference value of the row, not always its running maximum: weights are
-// 2^(scale (s - m)), and O and l are rescaled only when the maximum has outgrown m by more than 2^60
-// (fp32 and bf16 weights, O and l have the exponents for that, and their relative rounding does not
-// depend on m), which is as good as never after a row's first tile.
+// 2^(scale (s - m)), and O and l are rescaled only when the maximum has outgrown m by more than 2^8, which
+// is seldom after a row's first tile (the relative rounding of weights, O and l does not depend on m).
+// A limit of 2^60 measured the same (383 us a prompt of 8192, 439 us 1000 tokens on 32768, either way) and
+// took 2^52 from the values that O can hold: it is not yet divided by l, so 2^8 L max |v| has to stay in fp32.
 //
 // Weights in the product with V: PARTS = 1 rounds them to bf16 (2^-9 relative, of the order of the
 // rounding of a bf16 output); PARTS = 3, for fp32 outputs, keeps 24 bits as three bf16 terms, each
@@ -53,7 +54,7 @@ constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTa
 constexpr int kTaSegment = 8;         // key tiles that O gathers (PARTS > 1; 16 instead: 6 % faster on 96
                                       // sequences behind two documents, and nearly twice as far off)
 constexpr int kTaSplitTiles = 16;     // key tiles of a split at least, where every split leaves partials
-constexpr float kTaGrowth = 60.f;     // log2 of the largest weight before a rescale
+constexpr float kTaGrowth = 8.f;      // log2 of the largest weight before a rescale
 
 template <int D, int PARTS>
 struct TaTile {
@@ -114,10 +115,11 @@ __device__ __forceinline__ bool ta_locate(const TileParams& p, int slot, TaPlace
   return w->q0 >= 0 && i >= 0 && i < w->n && w->q0 + i < p.total_q;  // (rows past those of q are recorded)
 }
 
-// 2^x of two numbers without the special-function unit, x <= 8: x = i + f with |f| <= 1/2 (i by adding
+// 2^x of two numbers without the special-function unit, x <= kTaGrowth: x = i + f with |f| <= 1/2 (i by adding
 // 1.5 * 2^23), 2^f as a cubic, i added to the exponent.  The cubic is 1 at 0 and fitted here to the
-// smallest relative error, 2^-13.3: a twentieth of the rounding of the weight to bf16 that follows.  At
-// and below -127 the sum of the exponents is zero and so is the result.
+// smallest relative error, 2^-13.3: a twentieth of the rounding of the weight to bf16 that follows.  x is
+// raised to -127, where the sum of the exponents is zero and so is the result (a subnormal just above).
+static_assert(kTaGrowth <= 126.f, "the exponent that ex2_poly adds to stays below 255");
 constexpr float kEx2C1 = 0.693282902f, kEx2C2 = 0.242210954f, kEx2C3 = 0.0550089292f;
 
 __device__ __forceinline__ void ex2_poly(uint64_t v, float& x, float& y) {
