@@ -5,9 +5,10 @@ import pytest
 import torch
 
 from gpu_helpers import check_device, launches_of
-from test_gpu_cache_ops import (DENSE, STREAM, Cache, check_evict, check_prefill, check_prefix, draw_mass, i32, queries,
-                                run_evict, run_prefill, run_prefix)
+from test_gpu_cache_ops import (DENSE, STREAM, Cache, check_evict, check_prefill, check_prefix, draw_mass, grow,
+                                i32, offs, queries, run_evict, run_prefill, run_prefix)
 from token_sparse_decode_b200 import binding as B
+from token_sparse_decode_b200.step import PrefillStep
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +169,79 @@ def test_values_near_the_largest_when_maxima_grow(gain):
     q = (u + 0.02 * queries(366, 70, 4, 64).float()).bfloat16()
     out = run_prefix(p, own, q, None, 1.0)  # tiles and the dense pass
     check_prefix(p, own, q, None, 1.0, out, seqs=(0, 1, 7, 69))
+
+
+# ----------------------------------------------------------------------------------- long rows
+
+def long_rows(L, sink=0, window=None):
+    """(mean of out / reference - 1, launches) of 640 query rows at the end of L positions, 4 heads on each of 8 KV heads:
+    as many CTAs as do not split a row for the SMs' sake.  The keys are small, so that every token weighs about
+    1 / L, and the values lie between 1 and 2, at another level in each of the 512 columns."""
+    g = torch.Generator(device="cuda").manual_seed(371)
+    hkv, d, n = 8, 64, 640
+    k, v = (torch.empty((L, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    level = torch.linspace(1, 1.75, hkv * d, device="cuda").view(hkv, d)
+    for h in range(hkv):
+        k[:, h] = (torch.randn((L, d), generator=g, device="cuda") * 0.05).bfloat16()
+        v[:, h] = (torch.rand((L, d), generator=g, device="cuda") * 0.25 + level[h]).bfloat16()
+    q = torch.randn((n, 4 * hkv, d), generator=g, device="cuda").bfloat16()
+    step = PrefillStep(k, v, i32([0, L]), L, L, 4 * hkv, [DENSE if window is None else STREAM] * hkv, sink, window or 0, 0.1, n)
+    out = torch.zeros_like(q)
+    got = launches_of(lambda: step(q, i32([0, n]), out))
+    check_device()
+    rows = torch.tensor([0, 1, 300, 635, 639], device="cuda")
+    p, t = (L - n + rows).repeat_interleave(4)[:, None], torch.arange(L, device="cuda")
+    hidden = t > p if window is None else (t > p) | ((t >= sink) & (t <= p - window))
+    rel = []
+    for h in range(hkv):
+        x = 0.1 * (q[rows, 4 * h:4 * h + 4].double().reshape(-1, d) @ k[:, h].double().T)  # [rows * 4, L]
+        ref = torch.softmax(x.masked_fill(hidden, -float("inf")), 1) @ v[:, h].double()
+        rel.append(out[rows, 4 * h:4 * h + 4].double().reshape(-1, d) / ref - 1)
+    rel = torch.stack(rel)
+    assert float(rel.abs().max()) <= 2 * 2.0 ** -8  # the rounding of the output and of its weights, a half step each
+    return float(rel.mean()), got
+
+
+@pytest.mark.parametrize("L,sink,window", [(100_000, 0, None), (300_000, 0, None), (300_000, 128, 280_000), (1_000_000, 0, None)])
+def test_prefill_of_long_rows_does_not_drift(L, sink, window):
+    """The product with V drops the bits below the accumulator's last, always towards zero: less than 2^-23 of it per
+    16 tokens, on 131072 tokens at most.  Weights and outputs are rounded to nearest: a column's outputs are
+    nearly the same and share their rounding, at most 2^-8 and 2^-8 / sqrt(3) in the mean square, so that the mean
+    over 512 columns stays within 4 x 1.0e-4 (four standard deviations).  A quarter of the weights come from a
+    cubic within 1e-4, in the row's sum as well."""
+    drift, got = long_rows(L, sink, window)
+    assert got == {"tile_attend_kernel": 1}
+    assert -(min(L, 131072) / 16 * 2.0 ** -23 + 5e-4) <= drift <= 5e-4, drift
+
+
+@pytest.mark.parametrize("rows,launches", [(360, {"tile_attend_kernel": 1, "tile_merge_kernel": 1}), (600, {"tile_attend_kernel": 1})])
+def test_prefill_of_long_rows_whose_maxima_grow(rows, launches):
+    # two CTAs of more than 131072 tokens per row, or one of all; beside them short rows and one that sees nothing
+    c = Cache(381, [300_000, 40, 0, 3000], 1, 64, room=3)
+    grow(c)
+    new = [5, 40, 2, rows]
+    q = queries(382, sum(new) + 2, 32, 64)
+    kv = c.kv()
+    ws = B.workspace(B.stream_prefill_workspace_size(kv, 32, q.shape[0], [DENSE], 0, 0), "cuda").fill_(255)
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    assert launches_of(lambda: B.stream_prefill(q.cuda(), kv, i32(offs(new)), [DENSE], 0, 0, 0.4, out, ws)) == launches
+    check_device()
+    check_prefill(c, q, new, [DENSE], 0, 0, 0.4, out.cpu(), rows=(0, 39, 150))
+
+
+def test_prefill_of_short_rows_in_a_cache_that_may_hold_long_ones():
+    c = Cache(383, [40, 2500, 1], 1, 64)
+    new = [40, 700, 1]
+    q = queries(384, sum(new) + 3, 32, 64)
+    kv = c.kv()
+    kv.max_len = 1 << 20
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = B.workspace(B.stream_prefill_workspace_size(kv, 32, q.shape[0], [DENSE], 0, 0), "cuda").fill_(255)
+    assert launches_of(lambda: B.stream_prefill(q.cuda(), kv, i32(offs(new)), [DENSE], 0, 0, 0.1, out, ws)) == {
+        "tile_attend_kernel": 1}
+    check_device()
+    check_prefill(c, q, new, [DENSE], 0, 0, 0.1, out.cpu(), rows=(0, 39, 300, 699))
+    again = torch.full_like(out, 7.0)
+    kv.max_len = c.max_len  # no room for partials asked for, and none used
+    B.stream_prefill(q.cuda(), kv, i32(offs(new)), [DENSE], 0, 0, 0.1, again, ws)
+    assert torch.equal(out, again)

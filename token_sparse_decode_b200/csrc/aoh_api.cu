@@ -1980,6 +1980,7 @@ int list_by_role(const aoh_kv_cache* kv, const uint8_t* roles, uint8_t* out) {
 
 struct TileWs {
   int slots, splits;
+  bool segments;  // room for O of rows with more key tiles than a segment
   size_t off_acc, total;
 };
 
@@ -2003,7 +2004,8 @@ TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, 
   }
   const int64_t ctas = std::max<int64_t>(1, int64_t(w.slots) * n_listed);
   w.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sm_count() / ctas, ceil_div(longest, bn) / (keep ? kTaSplitTiles : 4)));
-  if (w.splits > 1 || keep) {
+  w.segments = keep || w.splits > 1 || ceil_div(longest, bn) > kTaSegmentLong;
+  if (w.segments) {
     const size_t rows = (size_t)w.splits * (size_t)ctas * 2 * 128;  // whole tiles
     w.off_acc = align256(sizeof(float) * 2 * rows);
     w.total = w.off_acc + align256(sizeof(float) * rows * kv->head_dim);
@@ -2027,6 +2029,7 @@ aoh_status bind_tiles(TileParams& tp, const void* q, int32_t Hq, const aoh_kv_ca
   tp.PT = PT;
   tp.total_q = (int)total_q;
   tp.splits = w.splits;
+  tp.segment = w.segments ? kTaSegmentLong : INT32_MAX;
   tp.slots = w.slots;
   // a positive factor: masked scores are -inf before they are scaled, and -inf * 0 is a NaN
   tp.scale_log2 = std::max(std::fabs(scale) * 1.4426950408889634f, 1.17549435e-38f);

@@ -27,10 +27,15 @@
 //
 // Weights in the product with V: PARTS = 1 rounds them to bf16 (2^-9 relative, of the order of the
 // rounding of a bf16 output); PARTS = 3, for fp32 outputs, keeps 24 bits as three bf16 terms, each
-// multiplied with V (two terms and key tiles of 128 were a tenth faster and twice as far off).  The
-// accumulation in TMEM drops the bits below the accumulator's last, always towards zero, which adds
-// up along a row (9e-6 after 3600 tokens): with PARTS = 3 a row's O is therefore added to its partial in
-// memory (which stays in L2) after every kTaSegment key tiles, and begins again from zero.
+// multiplied with V (two terms and key tiles of 128 were a tenth faster and twice as far off).  Two terms for
+// bf16 outputs, too, took 490 us instead of 383 on a prompt of 8192 and 566 instead of 439 on 1000 tokens behind
+// 31768; with one the output is 1.3 to 1.4 times as far from the exact value as its own rounding takes it.
+//
+// Segments.  The accumulation in TMEM drops the bits below the accumulator's last, always towards zero, which
+// adds up along a row (9e-6 after 3600 tokens of random values, 6e-3 after a million of one sign).  A
+// row's O is therefore added to a partial in memory (which stays in L2) after every segment of key tiles,
+// and begins again from zero: after 512 tokens with PARTS = 3, after 131072 with PARTS = 1, where shorter rows
+// need no partial.
 //
 // Bound and measured (B200).  Long rows run at the pace of one tile's chain: scores from TMEM, maximum,
 // exponentials (a quarter of them on the FMA pipe), weights back, then the products of both tiles: 3050
@@ -51,8 +56,9 @@ constexpr int kTaRegsSoftmax = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 re
 constexpr int kTaRegsOther = 88;
 constexpr int kTaRegsLaunch = 168;
 constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
-constexpr int kTaSegment = 8;         // key tiles that O gathers (PARTS > 1; 16 instead: 6 % faster on 96
-                                      // sequences behind two documents, and nearly twice as far off)
+constexpr int kTaSegment = 8;         // key tiles of a segment, PARTS = 3 (16 instead: 6 % faster on 96 sequences
+                                      // behind two documents, and nearly twice as far off)
+constexpr int kTaSegmentLong = 1024;  // the same, PARTS = 1
 constexpr int kTaSplitTiles = 16;     // key tiles of a split at least, where every split leaves partials
 constexpr float kTaGrowth = 8.f;      // log2 of the largest weight before a rescale
 
@@ -79,6 +85,7 @@ struct alignas(64) TileParams {
   float4* part_acc;          // [splits][tiles][D / 4][128]
   int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed, slots;
   int32_t causal;            // 0: every row sees the whole group
+  int32_t segment;           // key tiles of a segment (PARTS = 1; more than any row has: no room for partials)
   float scale_log2;          // > 0; a negative scale negates Q in the product
   uint32_t neg;
   uint8_t heads[kMaxHeads];
@@ -214,8 +221,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const int n_all = some ? a1 + max(0, b1 - b0) : 0;
   const int j_lo = (int)((int64_t)n_all * blockIdx.y / p.splits);
   const int n_it = (int)((int64_t)n_all * (blockIdx.y + 1) / p.splits) - j_lo;
-  // O is taken out after key tile j
-  auto last_of = [&](int j) { return j + 1 == n_it || (PARTS > 1 && (j + 1) % kTaSegment == 0); };
+  const int segment = PARTS > 1 ? kTaSegment : p.segment;
   auto key_tile = [&](int j) { return (j_lo + j < a1 ? j_lo + j : b0 + j_lo + j - a1) * BN; };
 
   tc_fence_before();
@@ -288,8 +294,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
         }
         __syncwarp();
         int sv = 1, ph = 0;  // stage and phase of V_j; K_{j+1} is in the next one
+        int left = segment;  // key tiles of this segment
         for (int j = 0; j < n_it; ++j) {
-          const bool more = j + 1 < n_it, last = last_of(j), first = PARTS > 1 ? j % kTaSegment == 0 : j == 0;
+          const bool more = j + 1 < n_it, first = left == segment, last = !more || left == 1;
+          left = left == 1 ? segment : left - 1;
           const int sk = sv + 1 == ST ? 0 : sv + 1, pk = sv + 1 == ST ? ph ^ 1 : ph;
           if (!warp_wait(bar_full(sv), ph, stop)) return;
           if (more && !warp_wait(bar_full(sk), pk, stop)) return;
@@ -344,7 +352,9 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     bool ok = true;
     const bool part = PARTS > 1 || p.splits > 1;
     float fac = 1.f;  // what the row's partial in memory is still to be scaled by
-    auto take_out = [&](bool have, bool add) {  // O and l of the row; add: to the partial written before
+    // O and l of the row; add: to the partial written before; last: of the row's segments
+    auto take_out = [&](bool have, bool add, bool last) {
+      const bool to_memory = PARTS > 1 || part || !last;
       const float inv = part ? 1.f : (l > 0.f ? 1.f / l : 0.f);
       const int64_t pt = ((int64_t)blockIdx.y * p.slots * p.n_listed + (int64_t)slot_id * p.n_listed + y) * 2 + t;
       float4* acc_out = p.part_acc + pt * (D / 4) * 128 + r;
@@ -363,16 +373,18 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (part) {
+        // A partial is written and read by the same thread.  (Two forms of the same sums: each instance spills
+        // half a kilobyte a thread with the other's.)
+        if (PARTS > 1) {
           float4 old[8];
-          if (PARTS > 1 && add)
+          if (add)
 #pragma unroll
             for (int e = 0; e < 8; ++e) old[e] = __ldcg(acc_out + (c / 4 + e) * 128);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             float4 v = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]),
                                    __uint_as_float(o[4 * e + 3]));
-            if (PARTS > 1 && add) {
+            if (add) {
               v.x = fmaf(old[e].x, fac, v.x);
               v.y = fmaf(old[e].y, fac, v.y);
               v.z = fmaf(old[e].z, fac, v.z);
@@ -380,6 +392,23 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
             }
             __stcg(acc_out + (c / 4 + e) * 128, v);
           }
+          continue;
+        }
+        if (add) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v = __ldcg(acc_out + (c / 4 + e) * 128);
+            o[4 * e] = __float_as_uint(fmaf(v.x, fac, __uint_as_float(o[4 * e])));
+            o[4 * e + 1] = __float_as_uint(fmaf(v.y, fac, __uint_as_float(o[4 * e + 1])));
+            o[4 * e + 2] = __float_as_uint(fmaf(v.z, fac, __uint_as_float(o[4 * e + 2])));
+            o[4 * e + 3] = __float_as_uint(fmaf(v.w, fac, __uint_as_float(o[4 * e + 3])));
+          }
+        }
+        if (to_memory) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            __stcg(acc_out + (c / 4 + e) * 128, make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                           __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -394,7 +423,7 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
         }
       }
       __syncwarp();
-      if (!part) {
+      if (!to_memory) {
         constexpr int LPR = D / 8;  // lanes per row
 #pragma unroll 4
         for (int k = 0; k < LPR; ++k) {
@@ -410,131 +439,142 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
       }
       fac = 1.f;
     };
-    if (t < tiles) {
-      for (int j = 0; j < n_it; ++j) {
-        if (!(ok = warp_wait(bar_s(t), j & 1, stop))) break;
-        tc_fence_after();
-        const int t0 = key_tile(j);
-        // (a warp without rows leaves P as it is: rows of a product do not mix)
-        const bool none = t0 > w_hi || (!dense && t0 >= p.sink && t0 + BN - 1 <= w_lo - p.window);
-        if (live && none) {
-          uint32_t z[32];
+    auto weigh = [&](int j, bool first) {  // the scores of key tile j become weights; first: of a segment
+      tc_fence_after();
+      const int t0 = key_tile(j);
+      // (a warp without rows leaves P as it is: rows of a product do not mix)
+      const bool none = t0 > w_hi || (!dense && t0 >= p.sink && t0 + BN - 1 <= w_lo - p.window);
+      if (live && none) {
+        uint32_t z[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) z[e] = 0;
+        for (int e = 0; e < 32; ++e) z[e] = 0;
 #pragma unroll
-          for (int c = 0; c < PARTS * BN / 2; c += 32) tmem_st32(s_t + c, z);
-          tmem_wait_st();
-        } else if (live) {
-          uint32_t s[BN];
+        for (int c = 0; c < PARTS * BN / 2; c += 32) tmem_st32(s_t + c, z);
+        tmem_wait_st();
+      } else if (live) {
+        uint32_t s[BN];
 #pragma unroll
-          for (int c = 0; c < BN; c += 32) tmem_ld32(s + c, s_t + c);
-          tmem_wait_ld();
-          const bool all = t0 + BN - 1 <= w_lo && (dense || t0 <= p.sink - BN || t0 > w_hi - p.window);
-          if (!all) {
-            const int hi = pos - t0, lo = dense ? -1 : pos - p.window - t0, sk = dense ? 0 : p.sink - t0;
+        for (int c = 0; c < BN; c += 32) tmem_ld32(s + c, s_t + c);
+        tmem_wait_ld();
+        const bool all = t0 + BN - 1 <= w_lo && (dense || t0 <= p.sink - BN || t0 > w_hi - p.window);
+        if (!all) {
+          // hidden: behind hi, and the `gap` tokens from sk on.  (Selects: as conditions joined by && and || these
+          // became a branch per token in some builds, 25 us more per CTA.)
+          const int hi = pos - t0, lo = dense ? -1 : pos - p.window - t0, sk = dense ? 0 : p.sink - t0;
+          const uint32_t gap = lo >= sk ? (uint32_t)lo - (uint32_t)sk + 1u : 0u;
 #pragma unroll
-            for (int c = 0; c < BN; ++c)
-              if (c > hi || (c <= lo && c >= sk)) s[c] = 0xff800000u;
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < BN; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool grow = (top - m) * sc > kTaGrowth;  // false while nothing has been seen
-          if (__any_sync(0xffffffffu, grow)) {
-            const float mn = grow ? top : m;
-            const float al = grow ? ex2((m - mn) * sc) : 1.f;
-            l *= al;
-            fac *= al;
-            m = mn;
-            if (PARTS > 1 ? j % kTaSegment != 0 : j > 0) {
-              const uint64_t al2 = f2(al, al);
-#pragma unroll
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, o_t + c);
-                tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  float x, y;
-                  f2_split(f2_mul(f2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), x, y);
-                  o[e] = __float_as_uint(x);
-                  o[e + 1] = __float_as_uint(y);
-                }
-                tmem_st32(o_t + c, o);
-              }
-            }
-          }
-          const float ms = m == -INFINITY ? 0.f : -m * sc;
-          const uint64_t ms2 = f2(ms, ms);
-          uint64_t sum = 0;
-          auto weights = [&](auto& w, int c0, int n) {  // of tokens c0 .. c0 + 2 n - 1
-#pragma unroll
-            for (int e = 0; e < n; ++e) {
-              const int c = c0 + 2 * e;
-              const uint64_t v2 = f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2);
-              float x, y;
-              if (PARTS == 1 && e % kTaPolyOf < kTaPoly) {
-                ex2_poly(v2, x, y);
-              } else {
-                f2_split(v2, x, y);
-                x = ex2(x);
-                y = ex2(y);
-              }
-              sum = f2_add(sum, f2(x, y));
-#pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
-                const uint32_t v = pack_bf16x2(x, y);
-                w[part][e] = v;
-                x -= bf16lo(v);
-                y -= bf16hi(v);
-              }
-            }
-          };
-          auto publish = [&](int h) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_p(t, h));
-          };
-          uint32_t w0[PARTS][C0 / 2];
-          weights(w0, 0, C0 / 2);
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int c = 0; c < C0 / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + c, w0[part] + c);
-          publish(0);
-          uint32_t w1[PARTS][(BN - C0) / 2];
-          weights(w1, C0, (BN - C0) / 2);
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-            for (int c = 0; c < (BN - C0) / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + C0 / 2 + c, w1[part] + c);
-          publish(1);
-          float x, y;
-          f2_split(sum, x, y);
-          l += x + y;
+          for (int c = 0; c < BN; ++c) s[c] = ((c > hi) | ((uint32_t)c - (uint32_t)sk < gap)) ? 0xff800000u : s[c];
         }
-        if (!live || none) {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < BN; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = max3(mx[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = (top - m) * sc > kTaGrowth;  // false while nothing has been seen
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? top : m;
+          const float al = grow ? ex2((m - mn) * sc) : 1.f;
+          l *= al;
+          fac *= al;
+          m = mn;
+          if (!first) {
+            const uint64_t al2 = f2(al, al);
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o, o_t + c);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float x, y;
+                f2_split(f2_mul(f2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), al2), x, y);
+                o[e] = __float_as_uint(x);
+                o[e + 1] = __float_as_uint(y);
+              }
+              tmem_st32(o_t + c, o);
+            }
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : -m * sc;
+        const uint64_t ms2 = f2(ms, ms);
+        uint64_t sum = 0;
+        auto weights = [&](auto& w, int c0, int n) {  // of tokens c0 .. c0 + 2 n - 1
+#pragma unroll
+          for (int e = 0; e < n; ++e) {
+            const int c = c0 + 2 * e;
+            const uint64_t v2 = f2_fma(f2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ms2);
+            float x, y;
+            if (PARTS == 1 && e % kTaPolyOf < kTaPoly) {
+              ex2_poly(v2, x, y);
+            } else {
+              f2_split(v2, x, y);
+              x = ex2(x);
+              y = ex2(y);
+            }
+            sum = f2_add(sum, f2(x, y));
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+              const uint32_t v = pack_bf16x2(x, y);
+              w[part][e] = v;
+              x -= bf16lo(v);
+              y -= bf16hi(v);
+            }
+          }
+        };
+        auto publish = [&](int h) {
+          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane < 2) mbar_arrive(bar_p(t, lane));
+          if (lane == 0) mbar_arrive(bar_p(t, h));
+        };
+        uint32_t w0[PARTS][C0 / 2];
+        weights(w0, 0, C0 / 2);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int c = 0; c < C0 / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + c, w0[part] + c);
+        publish(0);
+        uint32_t w1[PARTS][(BN - C0) / 2];
+        weights(w1, C0, (BN - C0) / 2);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int c = 0; c < (BN - C0) / 2; c += 16) tmem_st16(s_t + part * (BN / 2) + C0 / 2 + c, w1[part] + c);
+        publish(1);
+        float x, y;
+        f2_split(sum, x, y);
+        l += x + y;
+      }
+      if (!live || none) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane < 2) mbar_arrive(bar_p(t, lane));
+      }
+    };
+    if (t < tiles) {
+      if (PARTS > 1) {
+        for (int j = 0; j < n_it; ++j) {
+          if (!(ok = warp_wait(bar_s(t), j & 1, stop))) break;
+          weigh(j, j % kTaSegment == 0);
+          if (j + 1 == n_it || (j + 1) % kTaSegment == 0) {
+            if (!(ok = warp_wait(bar_o(t), (j / kTaSegment) & 1, stop))) break;
+            tc_fence_after();
+            if (live) take_out(true, j >= kTaSegment, false);
+          }
         }
-        if (PARTS > 1 && last_of(j)) {
-          if (!(ok = warp_wait(bar_o(t), (j / kTaSegment) & 1, stop))) break;
+      } else {
+        int j = 0;
+        for (int sg = 0; j < n_it && ok; ++sg) {
+          const int j_seg = j, j_end = n_it - j > segment ? j + segment : n_it;
+          for (; j < j_end && (ok = warp_wait(bar_s(t), j & 1, stop)); ++j) weigh(j, j == j_seg);
+          ok = ok && warp_wait(bar_o(t), sg & 1, stop);
           tc_fence_after();
-          if (live) take_out(true, j >= kTaSegment);
+          if (ok && live) take_out(true, sg > 0, j == n_it);
         }
       }
-      if (PARTS == 1 && n_it > 0) {
-        ok = ok && warp_wait(bar_o(t), 0, stop);
-        tc_fence_after();
-        if (ok && live) take_out(true, false);
-      }
-      if (n_it == 0 && live) take_out(false, false);
+      if (n_it == 0 && live) take_out(false, false, true);
     }
   }
   __syncwarp();
