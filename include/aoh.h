@@ -561,8 +561,8 @@ size_t aoh_prefix_decode_workspace_size(const aoh_kv_cache* prefix, const aoh_kv
  *   decay      finite (1: a plain sum)
  *   mass_in    device fp32 [Hkv][total_tokens] (layout of aoh_tip_score's scores), or
  *              NULL (zeros)
- *   mass_out   same layout, may be mass_in itself; entries of tokens outside every
- *              [0, L_b) are left as they are
+ *   mass_out   same layout, may be mass_in itself (any other overlap is refused); entries of
+ *              tokens outside every [0, L_b) are left as they are
  *   out        device fp32 [B][n_q_heads][d], 16-byte aligned
  *   workspace  device, 256-byte aligned, >= aoh_accum_decode_workspace_size
  *              bytes (any contents)

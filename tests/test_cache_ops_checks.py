@@ -19,3 +19,11 @@ def test_a_cache_without_rows_needs_no_address(lib):
         assert accum(lib, bad) == INVALID and prefill(lib, bad) == INVALID
         assert prefix(lib, bad, kv()) == INVALID and prefix(lib, kv(), bad) == INVALID
         assert evict(lib, bad, other()) == INVALID and evict(lib, kv(), other(**{gone: None})) == INVALID
+
+
+def test_accumulated_weights_overlap_wholly_or_not_at_all(lib):
+    n = 4 * 8 * 2000  # bytes
+    for mi in (0x100000 - n + 4, 0x100000 - 4, 0x100000 + 4, 0x100000 + n - 4):
+        assert accum(lib, kv(), mi=mi, mo=0x100000) == INVALID, hex(mi)
+    for mi in (None, 0x100000 - n, 0x100000, 0x100000 + n):  # the workspace is what is refused
+        assert accum(lib, kv(), mi=mi, mo=0x100000, ws=None) == WS, mi

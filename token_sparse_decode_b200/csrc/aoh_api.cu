@@ -2256,6 +2256,8 @@ aoh_status aoh_accum_decode(const void* q, int32_t n_q_heads, const aoh_kv_cache
   if (!std::isfinite(scale) || !std::isfinite(decay)) return AOH_ERR_INVALID_ARG;
   if (kv->batch == 0) return AOH_OK;
   if (!q || !out || (!mass_out && kv->total_tokens > 0)) return AOH_ERR_INVALID_ARG;
+  const uintptr_t mass_bytes = 4 * (uintptr_t)kv->total_tokens * kv->n_kv_heads;
+  if (mass_in && mass_in != mass_out && overlap(mass_in, mass_bytes, mass_out, mass_bytes)) return AOH_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out)) return AOH_ERR_ALIGNMENT;
   const AccumWs w = accum_ws(kv, n_q_heads);
   if (!ws_ok(workspace, workspace_bytes, w.total)) return AOH_ERR_WORKSPACE;
