@@ -1,6 +1,9 @@
 """More host-side checks of the cache operators (no device needed)."""
 
+import pytest
+
 from test_cache_ops_refusals import INVALID, WS, accum, evict, kv, lib, other, prefill, prefix  # noqa: F401 (lib: fixture)
+from token_sparse_decode_b200.step import EvictDecodeStep
 
 
 def empty(**kw):
@@ -27,3 +30,9 @@ def test_accumulated_weights_overlap_wholly_or_not_at_all(lib):
         assert accum(lib, kv(), mi=mi, mo=0x100000) == INVALID, hex(mi)
     for mi in (None, 0x100000 - n, 0x100000, 0x100000 + n):  # the workspace is what is refused
         assert accum(lib, kv(), mi=mi, mo=0x100000, ws=None) == WS, mi
+
+
+@pytest.mark.parametrize("budget,sink,recent", [(64, 40, 25), (0, 0, 0), (64, -1, 4), (64, 4, -1)])
+def test_bounded_decode_refuses_a_budget_that_eviction_would_refuse(budget, sink, recent):
+    with pytest.raises(ValueError):
+        EvictDecodeStep(2, 8, 2, 64, 1e4, budget, 8, sink, recent, 0.1)

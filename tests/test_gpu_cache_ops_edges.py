@@ -8,7 +8,7 @@ from gpu_helpers import check_device, launches_of
 from test_gpu_cache_ops import (DENSE, STREAM, Cache, check_evict, check_prefill, check_prefix, draw_mass, grow,
                                 i32, offs, queries, run_evict, run_prefill, run_prefix)
 from token_sparse_decode_b200 import binding as B
-from token_sparse_decode_b200.step import PrefillStep
+from token_sparse_decode_b200.step import EvictDecodeStep, PrefillStep
 
 pytestmark = pytest.mark.gpu
 
@@ -245,3 +245,37 @@ def test_prefill_of_short_rows_in_a_cache_that_may_hold_long_ones():
     kv.max_len = c.max_len  # no room for partials asked for, and none used
     B.stream_prefill(q.cuda(), kv, i32(offs(new)), [DENSE], 0, 0, 0.1, again, ws)
     assert torch.equal(out, again)
+
+
+# ----------------------------------------------------------------------------------- bounded cache
+
+def test_bounded_decode_captured_over_a_whole_cycle():
+    """Two equal steps, one eager, one captured from a full buffer over 2 * slack calls and replayed."""
+    slack, nb, hq, hkv, d = 3, 2, 4, 2, 64
+    steps = [EvictDecodeStep(nb, hq, hkv, d, 1e4, 12, slack, 2, 4, 0.125, 0.9) for _ in range(2)]
+    new = [tuple(queries(400 + 3 * i + k, nb, h, d).cuda() for k, h in enumerate((hq, hkv, hkv))) for i in range(30)]
+    it = 0
+    while not (steps[0].held == steps[0].cap and steps[0].cur == 0 and it > slack):
+        for s in steps:
+            s(*new[it])
+        it += 1
+    eager, captured = steps
+    static = [tuple(torch.zeros_like(x) for x in new[0]) for _ in range(2 * slack)]
+    outs = [torch.zeros_like(captured.out) for _ in range(2 * slack)]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        for x, o in zip(static, outs):
+            o.copy_(captured(*x))
+    assert captured.held == captured.cap and captured.cur == 0
+    for _ in range(2):
+        for i, x in enumerate(static):
+            for a, b in zip(x, new[it + i]):
+                a.copy_(b)
+        graph.replay()
+        for i in range(2 * slack):
+            assert torch.equal(eager(*new[it + i]), outs[i])
+        it += 2 * slack
+        assert torch.equal(eager.positions, captured.positions) and torch.equal(eager.mass, captured.mass)
+        assert torch.equal(eager.k[eager.cur], captured.k[captured.cur])
+    check_device()

@@ -366,12 +366,18 @@ class EvictDecodeStep:
     attention weights to ``mass``.  When a sequence may be at ``budget + slack`` rows the cache is
     first thinned to ``budget`` rows per head into the second of two buffers, which then takes its place.  ``load`` fills the
     cache from a prompt's rows and weights.
+
+    Rows are counted, and the buffer is chosen, on the host: a captured call replays the step that it was, on the
+    buffer that it had.  A graph that is replayed holds whole cycles (2 * slack calls from a state with
+    ``held == cap`` lead back to it).
     """
 
     def __init__(self, batch: int, n_q_heads: int, n_kv_heads: int, head_dim: int, theta: float, budget: int, slack: int,
                  sink: int, recent: int, scale: float, decay: float = 1.0, device="cuda"):
         if slack < 1:
             raise ValueError("EvictDecodeStep: slack must be at least 1")
+        if budget < 1 or sink < 0 or recent < 0 or sink + recent > budget:
+            raise ValueError(f"EvictDecodeStep: sink {sink} and recent {recent} do not fit a budget of {budget}")
         self.dev = torch.device(device)
         self.B, self.Hq, self.Hkv, self.d = batch, n_q_heads, n_kv_heads, head_dim
         self.theta, self.scale, self.decay = float(theta), float(scale), float(decay)
