@@ -1,5 +1,9 @@
 """More host-side checks of the cache operators (no device needed)."""
 
+import re
+from pathlib import Path
+
+import numpy as np
 import pytest
 
 from test_cache_ops_refusals import INVALID, WS, accum, evict, kv, lib, other, prefill, prefix  # noqa: F401 (lib: fixture)
@@ -36,3 +40,16 @@ def test_accumulated_weights_overlap_wholly_or_not_at_all(lib):
 def test_bounded_decode_refuses_a_budget_that_eviction_would_refuse(budget, sink, recent):
     with pytest.raises(ValueError):
         EvictDecodeStep(2, 8, 2, 64, 1e4, budget, 8, sink, recent, 0.1)
+
+
+def test_the_cubic_of_the_tile_softmax_against_exp2():
+    """2^f on [-1/2, 1/2] with the kernel's constants, in fp32 as the kernel adds it up, against exp2: within 2^-13.2
+    (the fit's 2^-13.3 and three roundings of 2^-24)."""
+    src = (Path(__file__).parent.parent / "token_sparse_decode_b200" / "csrc" / "tile_attend.cuh").read_text()
+    c1, c2, c3 = (np.float32(re.search(rf"kEx2C{i} = ([0-9.]+)f", src).group(1)) for i in (1, 2, 3))
+    f = np.linspace(-0.5, 0.5, 200_001, dtype=np.float32)
+    r = c3
+    for c in (c2, c1, np.float32(1)):
+        r = (np.float64(r) * f + c).astype(np.float32)  # one rounding, as an fma
+    err = np.abs(r.astype(np.float64) / np.exp2(f.astype(np.float64)) - 1)
+    assert err.max() <= 2.0 ** -13.2 and err[f == 0] == 0
