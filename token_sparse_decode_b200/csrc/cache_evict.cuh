@@ -92,6 +92,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictPa
   const int off = p.offsets[b], cap = p.offsets[b + 1] - off;
   const int kept = p.count[(int64_t)b * p.Hkv + g];
   const int doff = p.doffsets[b], dcap = p.doffsets[b + 1] - doff;
+  // the list is padded to the budget, so that its loads need not wait for the count's
+  const int32_t* lst = p.idx + ((int64_t)b * p.Hkv + g) * p.budget;
+  const int j0 = blockIdx.x * kEvictRows, ch = (tid % LPR) * 8, r0 = tid / LPR;
+  int pos[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int j = j0 + i * RPP + r0;
+    pos[i] = j < p.budget ? lst[j] : -1;
+  }
   const bool region = dcap >= 0 && doff >= 0 && (int64_t)doff + dcap <= p.dT;
   const int n = region && kept <= dcap ? kept : 0;  // rows moved: all or none
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
@@ -99,23 +108,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_copy_kernel(const EvictPa
     p.dlengths[b] = n;
   }
   if (!region) return;
-  const int j0 = blockIdx.x * kEvictRows;
   if (p.dmass) {  // slots past the kept rows start without weight
     float* dm = p.dmass + (int64_t)g * p.dT + doff;
     for (int j = n + blockIdx.x * kEvictThreads + tid; j < dcap; j += gridDim.x * kEvictThreads) dm[j] = 0.f;
   }
   if (j0 >= n) return;
-  const int32_t* lst = p.idx + ((int64_t)b * p.Hkv + g) * p.budget;
-  const int ch = (tid % LPR) * 8, r0 = tid / LPR;
-  int pos[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int j = j0 + i * RPP + r0;
-    pos[i] = j < n ? lst[j] : -1;
-    if (j < n && (pos[i] < 0 || pos[i] >= cap)) {
-      record_error(kCheckPosition, b, g, pos[i]);
-      pos[i] = -1;
-    }
+    if (j < n && (pos[i] < 0 || pos[i] >= cap)) record_error(kCheckPosition, b, g, pos[i]);
+    if (j >= n || pos[i] >= cap) pos[i] = -1;
   }
   const uint16_t* kb = p.k + (int64_t)off * p.stride_tok + (int64_t)p.slot[g] * p.stride_head + ch;
   const uint16_t* vb = p.v + (int64_t)off * p.stride_tok + (int64_t)p.slot[g] * p.stride_head + ch;
