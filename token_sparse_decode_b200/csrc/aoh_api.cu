@@ -2178,7 +2178,6 @@ aoh_status aoh_stream_prefill(const void* q, int32_t n_q_heads, const aoh_kv_cac
   tp.out = static_cast<uint16_t*>(out);
   tp.sink = sink;
   tp.window = window;
-  tp.causal = 1;
   memcpy(tp.roles, roles, kv->n_kv_heads);
   cudaStream_t st = as_stream(stream);
   s = kv->head_dim == 128 ? launch_tiles<128, 1>(tp, w, n_listed, st) : launch_tiles<64, 1>(tp, w, n_listed, st);
@@ -2233,7 +2232,6 @@ aoh_status aoh_prefix_decode(const void* q, int32_t n_q_heads, const aoh_kv_cach
   if ((s = bind_tiles(tp, q, n_q_heads, prefix, seq_start, kv->batch, scale, w.tiles, ws + w.off_tiles,
                       TaTile<128, 3>::BN)) != AOH_OK)
     return s;
-  memset(tp.roles, AOH_ROLE_DENSE, kv->n_kv_heads);
   s = kv->head_dim == 128 ? launch_tiles<128, 3>(tp, w.tiles, n_listed, st) : launch_tiles<64, 3>(tp, w.tiles, n_listed, st);
   if (s != AOH_OK || (s = count_launch(AOH_KERNEL_TILE_ATTEND, st)) != AOH_OK) return s;
   // the sequences' own tokens, beside the tiles on SMs that these leave; what one CTA finishes of them

@@ -84,7 +84,6 @@ struct alignas(64) TileParams {
   float2* part_ml;           // (m, l) [splits][tiles][128], m times scale_log2
   float4* part_acc;          // [splits][tiles][D / 4][128]
   int32_t B, Hq, G, PT, total_q, sink, window, splits, n_listed, slots;
-  int32_t causal;            // 0: every row sees the whole group
   int32_t segment;           // key tiles of a segment (PARTS = 1; more than any row has: no room for partials)
   float scale_log2;          // > 0; a negative scale negates Q in the product
   uint32_t neg;
@@ -203,15 +202,16 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
   const bool some = ta_locate(p, slot_id, &at);
   const int b = at.b, i0 = at.i0, n = at.n, q0 = at.q0, off = at.off, L = at.L;
   const int g = p.heads[y];
-  const bool dense = p.roles[g] == 1;
+  constexpr bool causal = PARTS == 1;  // rows of a shared prefix see all of it
+  const bool dense = !causal || p.roles[g] == 1;
   const int PT = p.PT;
   // tokens of this CTA (one minimum of a difference: min(min(2 PT, n - i0), total_q - q0 - i0) came out of
   // nvcc 12.9 without its second term)
   const int row_end = min(q0 + n, p.total_q), np = min(row_end - (q0 + i0), 2 * PT);
   const int tiles = !some ? 0 : np > PT ? 2 : 1;
   // key tiles that some row sees: [0, a1) and [b0, b1)
-  const int p_lo = p.causal ? max(L - n + i0, -1) : L - 1;
-  const int p_hi = p.causal ? max(L - n + i0 + np - 1, -1) : L - 1;
+  const int p_lo = causal ? max(L - n + i0, -1) : L - 1;
+  const int p_hi = causal ? max(L - n + i0 + np - 1, -1) : L - 1;
   int a1 = 0, b0 = 0;
   const int b1 = (p_hi + BN) / BN;  // ceil((p_hi + 1) / BN)
   if (!dense) {
@@ -340,10 +340,10 @@ __global__ void __launch_bounds__(kTaThreads, 1) tile_attend_kernel(const __grid
     const int tok = t * PT + r / p.G;
     const bool valid = r < PT * p.G && tok < np;
     const bool live = t < tiles && wr < PT * p.G && t * PT + wr / p.G < np;  // some row of the warp exists
-    const int pos = p.causal ? max(L - n + i0 + tok, -1) : L - 1;
+    const int pos = causal ? max(L - n + i0 + tok, -1) : L - 1;
     const int w_tok_hi = min(t * PT + min(wr + 31, PT * p.G - 1) / p.G, np - 1);
-    const int w_lo = p.causal ? max(L - n + i0 + t * PT + wr / p.G, -1) : L - 1;
-    const int w_hi = p.causal ? max(L - n + i0 + w_tok_hi, -1) : L - 1;
+    const int w_lo = causal ? max(L - n + i0 + t * PT + wr / p.G, -1) : L - 1;
+    const int w_hi = causal ? max(L - n + i0 + w_tok_hi, -1) : L - 1;
     const float sc = p.scale_log2;
     const uint64_t sc2 = f2(sc, sc);
     const uint32_t lanes = tmem + ((uint32_t)(wr & 96) << 16);
