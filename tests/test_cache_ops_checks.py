@@ -5,8 +5,10 @@ from pathlib import Path
 
 import numpy as np
 import pytest
+import torch
 
 from test_cache_ops_refusals import INVALID, WS, accum, evict, kv, lib, other, prefill, prefix  # noqa: F401 (lib: fixture)
+from token_sparse_decode_b200 import binding as B
 from token_sparse_decode_b200.step import EvictDecodeStep
 
 
@@ -53,3 +55,40 @@ def test_the_cubic_of_the_tile_softmax_against_exp2():
         r = (np.float64(r) * f + c).astype(np.float32)  # one rounding, as an fma
     err = np.abs(r.astype(np.float64) / np.exp2(f.astype(np.float64)) - 1)
     assert err.max() <= 2.0 ** -13.2 and err[f == 0] == 0
+
+
+class OnDevice:
+    """What make_kv looks at of a CUDA tensor."""
+
+    is_cuda = True
+
+    def __init__(self, dev, dtype, *shape):
+        self.dev, self.dtype, self.shape = dev, dtype, shape
+
+    def get_device(self):
+        return self.dev
+
+    def stride(self, i=None):
+        s = (self.shape[1] * self.shape[2], self.shape[2], 1)
+        return s if i is None else s[i]
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def data_ptr(self):
+        return 0x10000
+
+
+@pytest.mark.parametrize("wrong", [None, "v", "offsets", "lengths", "k_dom"])
+def test_a_cache_is_on_one_device(wrong):
+    at = {n: int(n == wrong) for n in ("v", "offsets", "lengths", "k_dom")}
+    bf, i32 = torch.bfloat16, torch.int32
+    k_dom = OnDevice(at["k_dom"], bf, 2, 10, 16)
+    k_dom.is_contiguous = lambda: True
+    args = (OnDevice(0, bf, 10, 2, 64), OnDevice(at["v"], bf, 10, 2, 64), OnDevice(at["offsets"], i32, 3), 5, 10, k_dom,
+            OnDevice(at["lengths"], i32, 2))
+    if wrong is None:
+        assert B.make_kv(*args).device == 0
+    else:
+        with pytest.raises(ValueError, match=wrong):
+            B.make_kv(*args)

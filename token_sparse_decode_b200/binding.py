@@ -183,6 +183,9 @@ def make_kv(k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor, max_len: in
     assert k.shape == v.shape and k.stride() == v.stride() and k.stride(2) == 1
     assert offsets.dtype == torch.int32 and offsets.is_cuda
     assert lengths is None or (lengths.dtype == torch.int32 and lengths.is_cuda)
+    for name, t in (("v", v), ("offsets", offsets), ("lengths", lengths), ("k_dom", k_dom)):
+        if t is not None and t.get_device() != k.get_device():
+            raise ValueError(f"make_kv: {name} is on cuda:{t.get_device()}, k on cuda:{k.get_device()}")
     kv = KVCache()
     slots = None if head_slot is None else (ctypes.c_uint8 * len(head_slot))(*[int(x) for x in head_slot])
     kv._keep = (k, v, offsets, k_dom, lengths, slots)  # raw pointers: keep their owners alive with the descriptor
