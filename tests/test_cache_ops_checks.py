@@ -92,3 +92,14 @@ def test_a_cache_is_on_one_device(wrong):
     else:
         with pytest.raises(ValueError, match=wrong):
             B.make_kv(*args)
+
+
+def test_append_at_checks_the_chunk_table(monkeypatch):
+    monkeypatch.setattr(B, "_device", lambda *caches: -1)  # where CPU tensors are
+    c = kv()
+    row = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    n = torch.zeros(2, dtype=torch.int32)
+    for idom, n_dom in ((torch.zeros((8, 4), dtype=torch.int64), 4), (torch.zeros((8, 3), dtype=torch.int32), 4),
+                        (torch.zeros((8, 4), dtype=torch.int32), 2 ** 32 + 4)):
+        with pytest.raises(ValueError, match="idom|n_dom"):
+            B.kv_append_at(None, row, row, 1e4, c, idom, n_dom, n, n.clone(), None)

@@ -448,7 +448,9 @@ def kv_append_at(q_new: Optional[torch.Tensor], k_new: torch.Tensor, v_new: torc
     if q_new is not None:
         shape, q_p = _want_q(fn, "q_new", q_new, n, d, dev)
         hq, qo_p = shape[1], _want(fn, "q_out", q_out, torch.bfloat16, shape, dev)
-    _check(fn, lib().aoh_kv_append_at(q_p, hq, k_p, v_p, theta, kv, _ptr(idom), n_dom, len_p, pos_p, qo_p,
+    _int32(fn, n_dom=n_dom)
+    idom_p = None if idom is None else _want(fn, "idom", idom, torch.int32, (kv.n_kv_heads, n_dom), dev)
+    _check(fn, lib().aoh_kv_append_at(q_p, hq, k_p, v_p, theta, kv, idom_p, n_dom, len_p, pos_p, qo_p,
                                       _raw_stream(stream, dev)))
 
 
