@@ -8,9 +8,10 @@ loss of any one mechanism would give:
     2^-24 of a logit around 1), each 16 tokens' product from zero and added in fp32, rounded to nearest: 3 to 4e-7.
     Bound 1e-6.  Two bf16 terms of a weight instead of three leave 2^-17 (rms 4.4e-6), sums gathered by the
     tensor cores 3e-6 after 900 tokens.
-  * shared prefixes through tiles: the same, and 3 x 32 products per segment of 512 tokens, each dropping half
-    of an accumulator's last bit on average (0.72 x 2^-24 of it, and O half as large as at the end): 2.1e-6, with
-    the above 2.6e-6 at most.  Bound 3e-6.  Two terms give 4.7e-6, no segments 9e-6 after 3600 tokens.
+  * shared prefixes through tiles: the same, and 3 x 16 products per segment of 256 tokens, each dropping half
+    of an accumulator's last bit on average (0.72 x 2^-24 of it, and O half as large as at the end): 1.03e-6, with
+    the above 1.1e-6.  Bound 1.3e-6.  Segments of 512 tokens give 1.7e-6, two terms 4.7e-6, no segments 9e-6 after
+    3600 tokens.
 """
 
 import math
@@ -77,6 +78,24 @@ def test_shared_prefixes_keep_fp32(d, G, plens, nb):
             vv = torch.cat([pv[poff[i]:poff[i + 1], g], v[off[b]:off[b + 1], g]])
             ref[b, g * G:(g + 1) * G] = softmax64(q[b, g * G:(g + 1) * G], kk, vv, 1 / math.sqrt(d))[0]
     assert off_by(res[0], ref) <= 3e-6
+
+
+@pytest.mark.parametrize("d,hkv,G,P,nb,own", [(128, 8, 4, 600, 64, 100), (128, 2, 4, 1765, 64, 100), (64, 1, 5, 1765, 33, 50),
+                                              (128, 2, 7, 8192, 40, 700), (64, 2, 4, 30000, 40, 0)])
+def test_shared_prefixes_of_every_length_keep_fp32(d, hkv, G, P, nb, own):
+    lens = [(37 * b) % (own + 1) for b in range(nb)]
+    off, T = [sum(lens[:i]) for i in range(nb + 1)], sum(lens)
+    pk, pv, k, v = normal(541, P, hkv, d), normal(542, P, hkv, d), normal(543, T, hkv, d), normal(544, T, hkv, d)
+    q = normal(545, nb, hkv * G, d)
+    step = PrefixDecodeStep(pk, pv, i32([0, P]), P, P, k, v, i32(off), max(lens), T, hkv * G, 1 / math.sqrt(d))
+    out = step(q)
+    check_device()
+    ref = torch.empty(q.shape, dtype=torch.float64, device="cuda")
+    for b in range(nb):
+        for g in range(hkv):
+            kk, vv = torch.cat([pk[:, g], k[off[b]:off[b + 1], g]]), torch.cat([pv[:, g], v[off[b]:off[b + 1], g]])
+            ref[b, g * G:(g + 1) * G] = softmax64(q[b, g * G:(g + 1) * G], kk, vv, 1 / math.sqrt(d))[0]
+    assert off_by(out, ref) <= 1.3e-6
 
 
 # ----------------------------------------------------------------------------------- very large caches

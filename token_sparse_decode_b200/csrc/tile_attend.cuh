@@ -34,7 +34,7 @@
 // Segments.  The accumulation in TMEM drops the bits below the accumulator's last, always towards zero, which
 // adds up along a row (9e-6 after 3600 tokens of random values, 6e-3 after a million of one sign).  A
 // row's O is therefore added to a partial in memory (which stays in L2) after every segment of key tiles,
-// and begins again from zero: after 512 tokens with PARTS = 3, after 131072 with PARTS = 1, where shorter rows
+// and begins again from zero: after 256 tokens with PARTS = 3, after 131072 with PARTS = 1, where shorter rows
 // need no partial.
 //
 // Bound and measured (B200).  Long rows run at the pace of one tile's chain: scores from TMEM, maximum,
@@ -56,8 +56,9 @@ constexpr int kTaRegsSoftmax = 208;   // 2 x 128 x 208 + 128 x 88 = 384 x 168 re
 constexpr int kTaRegsOther = 88;
 constexpr int kTaRegsLaunch = 168;
 constexpr int kTaPoly = 1, kTaPolyOf = 4;  // of kTaPolyOf pairs of weights, kTaPoly come from the FMA pipe
-constexpr int kTaSegment = 8;         // key tiles of a segment, PARTS = 3 (16 instead: 6 % faster on 96 sequences
-                                      // behind two documents, and nearly twice as far off)
+constexpr int kTaSegment = 4;         // key tiles of a segment, PARTS = 3: 9.5e-7 off (fp32 torch operations: 2e-7 to
+                                      // 3e-6).  8: 1.7e-6, 131 us instead of 142 on 96 sequences behind two documents
+                                      // and the same on 64 behind 8192 tokens; 2: 5.6e-7, 174 us
 constexpr int kTaSegmentLong = 1024;  // the same, PARTS = 1
 constexpr int kTaSplitTiles = 16;     // key tiles of a split at least, where every split leaves partials
 constexpr float kTaGrowth = 8.f;      // log2 of the largest weight before a rescale
