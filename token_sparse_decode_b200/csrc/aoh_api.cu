@@ -1986,8 +1986,9 @@ struct TileWs {
 
 // The grid of a tile call: a slot per two tiles of rows of every group, times the heads, times as
 // many splits of the key range as give every SM a CTA, of at least four key tiles each, or sixteen where every
-// split leaves partials anyway (64 sequences behind 8192 tokens, with the pass over their
-// own tokens on the other SMs: 18 splits 77 us, 10 68 us, 8 66 us).
+// split leaves partials anyway (64 sequences behind 8192 tokens on 8 heads, with the pass over their
+// own tokens on the other SMs: 18 splits 77 us, 10 68 us, 8 66 us; with fewer heads, or few own tokens,
+// it leaves SMs idle: 33 sequences behind 1765 tokens on one head take 50 us with 2 CTAs).
 TileWs tile_ws(const aoh_kv_cache* kv, int32_t Hq, int64_t total_q, int groups, const uint8_t* roles, int32_t sink,
                int32_t window, int bn, bool keep) {
   TileWs w{};

@@ -11,10 +11,12 @@
 //                      keys in registers: protected positions before every weight, a NaN as the lightest;
 //   evict_key_kernel and the library's select (longer rows): the same with the keys in memory;
 //   evict_copy_kernel  moves the rows.
-// Measured: 32 sequences of 700 to 4500 x 8 heads to 2048 rows in 98 us, the copy 79 us of it (6.7 TB/s
-// read and written, the measured copy rate); two of 65536 to 8192 in 41 us, copy 24, select 17.
-// All of it is bound by memory: 4 bytes per (head, position) for the weights and 8 d + 8 per
-// kept row read and written once.
+// Measured: 32 sequences of 700 to 4500 x 8 heads to 2048 rows in 94 us, the copy 75 us of it (6.5 TB/s
+// read and written, the measured copy rate); two of 65536 to 8192 in 44 us in a long run, 38 in a short one: copy
+// 24, the rest the select, which takes four cluster barriers.  Rows above 131072 positions take six launches: one of
+// 200000 x 8 heads to 8192 in 48 us, of 300000 in 157, of a million in 464.
+// The copy is bound by memory: 8 d + 8 bytes per kept row read and written once; the selects by
+// latency, beside 4 bytes per (head, position) for the weights.
 #pragma once
 
 #include "select_cluster.cuh"

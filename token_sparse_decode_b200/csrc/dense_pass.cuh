@@ -19,9 +19,10 @@
 // fp32 weights, and every sub-tile's product starts from zero and is added by the FMA units: the
 // tensor cores' own accumulation rounds towards zero, 3e-6 along 900 tokens.
 //
-// Bound by the K / V bytes.  Measured (B200): 131072 tokens x 8 heads, d 128 in 90 us, 5.96 TB/s (91 % of
-// the measured copy rate); 48 sequences of 1 to 8000 x 4 heads in 71 us, 5.5 TB/s (a grid of fixed chunks
-// fed by cp.async took 120 and 91 us).
+// Bound by the K / V bytes with up to 16 query rows.  Measured (B200): 131072 tokens x 8 heads, d 128 in 90 us,
+// 5.96 TB/s (91 % of the measured copy rate); 48 sequences of 1 to 8000 x 4 heads in 71 us, 5.5 TB/s (a grid of
+// fixed chunks fed by cp.async took 120 and 91 us).  More query rows on one KV head, 8 x 131072 tokens, d 128: 8
+// rows 99 us, 16 rows 109 us (4.9 TB/s); 17 to 32 rows, four times the products per byte, 191 us (2.8 TB/s).
 #pragma once
 
 #include <cuda.h>

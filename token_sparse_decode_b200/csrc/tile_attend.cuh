@@ -40,9 +40,10 @@
 // Bound and measured (B200).  Long rows run at the pace of one tile's chain: scores from TMEM, maximum,
 // exponentials (a quarter of them on the FMA pipe), weights back, then the products of both tiles: 3050
 // cycles per 128 keys and two tiles where the products alone take 2048.  1000 new tokens on 32768
-// (32 heads on 8, d 128): 440 us, 1200 TFLOP/s on 128 of 148 SMs; a prompt of 8192 with 2 of 8 groups
-// retrieval heads: 386 us, 1175 TFLOP/s; ragged prompts of 301 to 2500: 90 us, 600 TFLOP/s (short CTAs:
-// setting up and taking out cost as much as five key tiles).
+// (32 heads on 8, d 128): 433 us, 1220 TFLOP/s on 128 of 148 SMs, and 505 us, 1050 TFLOP/s in a long run at the
+// power limit; a prompt of 8192 with 2 of 8 groups retrieval heads: 382 us, 1186 TFLOP/s, and 445; ragged
+// prompts of 301 to 2500: 91 us, 585 TFLOP/s (short CTAs: setting up and taking out cost as much as five
+// key tiles).  96 sequences behind two documents of 20011 to 32768: 142 us with their own tokens.
 #pragma once
 
 #include <type_traits>
